@@ -70,6 +70,9 @@ typedef enum moe_status {
 
 typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
 
+/* Block-scaled element formats (see moe_mx_quantize): 8 and 4 bits. */
+typedef enum moe_mx_format { MOE_MX_E4M3 = 0, MOE_MX_E2M1 = 1 } moe_mx_format;
+
 typedef struct moe_dims {
   int64_t T;    /* tokens */
   int32_t d;    /* model width */
@@ -587,6 +590,125 @@ moe_status moe_shuffle_plan(int64_t T, int32_t k, int32_t E, int32_t G,
 moe_status moe_route_flips(int64_t T, int32_t k, int32_t E, const int32_t* topk_idx_a,
                            const int32_t* topk_idx_b, int32_t* flips, int32_t* n_flips,
                            void* stream);
+
+/*
+ * The norm in front of the layer and the layer's experts in low precision, for
+ * transformer blocks that keep their expert weights in 4 bits when they serve.
+ *
+ * Block-scaled rows (OCP Microscaling Formats).  A row of n values (n % 64 ==
+ * 0) is n elements and one scale byte per 32 of them: element i of block b
+ * stands for element * 2^(s[b] - 127); s = 255 makes every value of the block
+ * NaN.  MOE_MX_E4M3: a byte per element (sign, 4 exponent bits, 3 fraction
+ * bits, largest 448, no infinity).  MOE_MX_E2M1: four bits per element (0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6 and their negatives), element 2i in the low half of byte i.
+ * A scale row is padded to whole words: 4 * ceil(n / 128) bytes
+ * (moe_mx_scale_cols); the calls below write the padding as 0 and read it
+ * against zero elements only, where 255 would still give NaN.
+ *
+ * Quantising: s is the smallest scale, at least 0, that leaves no element
+ * above the format's largest; elements are rounded to nearest, ties to even.
+ * A block with a NaN or an infinity in it gets s = 255 (its elements are not
+ * specified).
+ *
+ * moe_mx_quantize: src [rows, cols] of src_dtype (MOE_F32 or MOE_BF16) to
+ *   q [rows, cols] bytes (E4M3) or [rows, cols / 2] bytes (E2M1) and
+ *   scale [rows, moe_mx_scale_cols(cols)].  Weights [E, out, in] are E * out
+ *   rows of `in` values.
+ * moe_mx_dequantize: the values, rounded to dst_dtype (exact in bf16 but for
+ *   its subnormal range and overflow), dst [rows, cols].
+ * moe_mx_scale_cols: [host] bytes of a scale row; 0 unless cols > 0 and
+ *   cols % 64 == 0.
+ */
+int32_t moe_mx_scale_cols(int32_t cols);
+moe_status moe_mx_quantize(int64_t rows, int32_t cols, int32_t src_dtype, const void* src,
+                           int32_t format, void* q, uint8_t* scale, void* stream);
+moe_status moe_mx_dequantize(int64_t rows, int32_t cols, int32_t format, const void* q,
+                             const uint8_t* scale, int32_t dst_dtype, void* dst, void* stream);
+
+/*
+ * moe_rmsnorm -- the residual's addition and the root-mean-square norm before
+ * the layer, with 8-bit rows for moe_expert_up_mx.
+ *
+ *   s[t] = x[t] + residual[t], rounded to act;
+ *   rstd[t] = 1 / sqrt(mean(s[t]^2) + eps);  y[t] = s[t] rstd[t] weight.
+ * The norm is of s as stored.  Squares and sums are fp32 (an |s| above about
+ * 1e19 overflows them: rstd 0).
+ * x [T,d] act; residual [T,d] act or NULL (s = x); weight [d] fp32; eps >= 0.
+ * sum [T,d] act or NULL: s.  It may be x or residual (in place).
+ * y [T,d] act or NULL; it may be x when sum is not.
+ * q [T,d] E4M3 and q_scale [T, moe_mx_scale_cols(d)], both or neither: the
+ *   fp32 y, quantised (not its act rounding).  y or q has to be given.
+ * rstd [T] fp32 or NULL (the backward pass reads it).
+ * Of dims, only T, d and act matter (E, f, k have to be valid).
+ *
+ * moe_rmsnorm_bwd -- with n = s rstd and g = dy weight:
+ *   dx = rstd (g - n mean(g n)) + dsum;  dweight = sum_t dy n.
+ * dy [T,d] act: gradient of y; s [T,d] act: the stored sum (x itself when
+ * there was no residual); rstd [T]; dsum [T,d] act or NULL: what reaches s
+ * from elsewhere (the residual stream).  dx [T,d] act: the gradient of x and of
+ * residual alike; it may be dy or dsum.  dweight [d] fp32, added in a fixed
+ * order.  Workspace: moe_rmsnorm_bwd_workspace_bytes (moe_workspace_bytes
+ * covers it).
+ */
+moe_status moe_rmsnorm(const moe_dims* dims, const void* x, const void* residual,
+                       const float* weight, float eps, void* sum, void* y, void* q,
+                       uint8_t* q_scale, float* rstd, void* stream);
+size_t moe_rmsnorm_bwd_workspace_bytes(const moe_dims* dims);   /* [host] 0 for invalid dims */
+moe_status moe_rmsnorm_bwd(const moe_dims* dims, const void* dy, const void* s,
+                           const float* weight, const float* rstd, const void* dsum, void* dx,
+                           float* dweight, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * The experts of a prompt in low precision: E4M3 rows against E2M1 weights,
+ * grouped by expert as moe_permute lays them out ([REVISIT] Sec. 2.1 SwiGLU;
+ * [COUPLING] Fig. 5 step 4).  The matrix instruction applies the scales and sums
+ * in fp32; within a block of 32 it aligns the products to the largest of them
+ * and keeps 14 bits below its power of two.
+ *
+ * moe_expert_up_mx, for each expert e over its rows p:
+ *   a[p] = x[r] W1[e]^T, b[p] = x[r] W3[e]^T, h[p] = silu(a[p]) b[p],
+ *   with r = src_token[p], or r = p when src_token is NULL; h is quantised
+ *   from fp32 to hq [T*k,f] E4M3 and h_scale [T*k, moe_mx_scale_cols(f)].
+ *   xq [T,d] E4M3 (src_token NULL: [T*k,d]) with x_scale; src_token [T*k] in
+ *   [0, T) or NULL; w1, w3 [E,f,d] E2M1 (d / 2 bytes a row) with w1_scale,
+ *   w3_scale [E, f, moe_mx_scale_cols(d)].
+ *   With src_token, T * d < 2^31 (else MOE_ERR_UNSUPPORTED).
+ * moe_expert_down_mx: y_perm[p] = h[p] W2[e]^T, [T*k,d] act; w2 [E,d,f] E2M1
+ *   with w2_scale [E, d, moe_mx_scale_cols(f)].
+ * expert_offsets [E+1] as moe_permute writes them; rows past offsets[E] of hq,
+ * h_scale and y_perm are left unchanged.  act is the type of y_perm alone.
+ * d, f <= 2^20, and fewer than 2^23 tiles of 256 x 128 outputs (else
+ * MOE_ERR_UNSUPPORTED).
+ */
+moe_status moe_expert_up_mx(const moe_dims* dims, const void* xq, const uint8_t* x_scale,
+                            const int32_t* src_token, const int32_t* expert_offsets,
+                            const void* w1, const uint8_t* w1_scale, const void* w3,
+                            const uint8_t* w3_scale, void* hq, uint8_t* h_scale, void* stream);
+moe_status moe_expert_down_mx(const moe_dims* dims, const void* hq, const uint8_t* h_scale,
+                              const int32_t* expert_offsets, const void* w2,
+                              const uint8_t* w2_scale, void* y_perm, void* stream);
+
+/*
+ * moe_token_swiglu -- the experts and the combine for a few tokens (decoding),
+ * straight from the router's table, with activations in act:
+ *   y[t] = sum_{j<k} gate[t,j] W2[e] (silu(W1[e] x[t]) (W3[e] x[t])),
+ *   e = topk_idx[t,j]; slots with an id outside [0, E) (dropped: -1) add
+ *   nothing.  The sum over slots is in slot order.
+ * x [T,d] act; topk_idx, topk_gate [T,k]; weights and scales as in
+ * moe_expert_up_mx and moe_expert_down_mx; y [T,d] act.  Products and sums are
+ * fp32; between the products h keeps 16 significant bits (bf16 layers) or 24.
+ * T * k <= MOE_TOKEN_MAX_SLOTS and d, f <= 2^20 (else MOE_ERR_UNSUPPORTED).
+ * Workspace: moe_token_swiglu_workspace_bytes(dims) (not covered by
+ * moe_workspace_bytes); 0 for dims that the call refuses, or T = 0.
+ */
+#define MOE_TOKEN_MAX_SLOTS 1024
+size_t moe_token_swiglu_workspace_bytes(const moe_dims* dims);   /* [host] */
+moe_status moe_token_swiglu(const moe_dims* dims, const void* x, const int32_t* topk_idx,
+                            const float* topk_gate, const void* w1, const uint8_t* w1_scale,
+                            const void* w3, const uint8_t* w3_scale, const void* w2,
+                            const uint8_t* w2_scale, void* y, void* workspace,
+                            size_t workspace_bytes, void* stream);
 
 /*
  * moe_placement_greedy -- [host] correlated expert placement ([COUPLING]

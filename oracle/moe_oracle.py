@@ -1029,3 +1029,98 @@ def dispatch_expand(recv, assign_row, pos):
             out[pos[t, j]] = recv[assign_row[t, j]]
     return out
 
+
+
+# ---------------------------------------------------------------------------
+# The norm before the layer, and block-scaled numbers (OCP Microscaling
+# Formats): 32 values share a power of two, elements are e4m3 or e2m1.
+# ---------------------------------------------------------------------------
+
+MX_BLOCK = 32
+MX_FORMATS = {"e4m3": (448.0, -6, 3), "e2m1": (6.0, 0, 1)}   # largest, lowest exponent, fraction bits
+
+
+def mx_scale_cols(n: int) -> int:
+    """bytes of a scale row of n values, padded to whole words"""
+    return 4 * (-(-n // 128))
+
+
+def mx_quantize(v, fmt):
+    """(element values, scale bytes without padding) of v [..., n]: the smallest
+    scale 2^(s - 127), s >= 0, that leaves no element above the format's
+    largest; nearest element, ties to even.  A block with a NaN or an infinity
+    has s = 255 and NaN elements."""
+    v = np.asarray(v, np.float64)
+    largest, low, frac = MX_FORMATS[fmt]
+    blocks = v.reshape(*v.shape[:-1], -1, MX_BLOCK)
+    bad = ~np.isfinite(blocks).all(-1)
+    amax = np.where(bad, 0.0, np.abs(blocks).max(-1))
+    s = np.zeros(amax.shape, np.int64)
+    for at in np.ndindex(amax.shape):
+        while s[at] < 254 and amax[at] > largest * 2.0 ** (s[at] - 127):
+            s[at] += 1
+    with np.errstate(invalid="ignore"):
+        u = blocks / 2.0 ** (s[..., None] - 127.0)
+        step = 2.0 ** (np.maximum(np.frexp(u)[1] - 1, low) - frac)
+        q = np.where(bad[..., None], np.nan, np.rint(u / step) * step)
+    return q.reshape(v.shape), np.where(bad, 255, s).astype(np.uint8)
+
+
+def mx_element_values(codes, fmt):
+    """fp64 values of e4m3 bytes, or of e2m1 bytes (two to a byte, low half first)"""
+    codes = np.asarray(codes).astype(np.int64)
+    if fmt == "e2m1":
+        codes = np.stack([codes & 15, codes >> 4], -1).reshape(*codes.shape[:-1], -1)
+        bias, fbits = 1, 1
+    else:
+        bias, fbits = 7, 3
+    top = 7 if fmt == "e4m3" else 3
+    sign = np.where((codes >> top) & 1, -1.0, 1.0)
+    exp = (codes >> fbits) & ((1 << (top - fbits)) - 1)
+    frac = (codes & ((1 << fbits) - 1)) / float(1 << fbits)
+    val = np.where(exp == 0, frac * 2.0 ** (1 - bias), (1 + frac) * 2.0 ** (exp - bias))
+    if fmt == "e4m3":
+        val = np.where((codes & 0x7F) == 0x7F, np.nan, val)
+    return sign * val
+
+
+def mx_values(elements, scale):
+    """values of elements [..., n] under scale bytes [..., >= n / 32]"""
+    elements = np.asarray(elements, np.float64)
+    n = elements.shape[-1] // MX_BLOCK
+    s = np.asarray(scale)[..., :n].astype(np.float64)
+    return elements * np.repeat(np.where(s == 255, np.nan, 2.0 ** (s - 127)), MX_BLOCK, -1)
+
+
+def rmsnorm(s, weight, eps):
+    """(y, rstd) of rows s [T, d] (the stored sum)"""
+    s = np.asarray(s, np.float64)
+    rstd = 1.0 / np.sqrt(np.mean(s * s, -1) + eps)
+    return s * rstd[:, None] * np.asarray(weight, np.float64), rstd
+
+
+def rmsnorm_bwd(dy, s, weight, eps, dsum=None):
+    """(dx, dweight): the Jacobian of rmsnorm applied to dy, plus dsum"""
+    dy, s, w = (np.asarray(a, np.float64) for a in (dy, s, weight))
+    _, rstd = rmsnorm(s, w, eps)
+    n, g = s * rstd[:, None], dy * w
+    dx = rstd[:, None] * (g - n * np.mean(g * n, -1, keepdims=True))
+    return (dx if dsum is None else dx + dsum), (dy * n).sum(0)
+
+
+def swiglu_hidden(x, w1, w3):
+    """(a, b, h) of rows x [n, d] with one expert's W1, W3 [f, d]"""
+    a, b = x @ np.asarray(w1).T, x @ np.asarray(w3).T
+    with np.errstate(over="ignore", invalid="ignore"):
+        return a, b, a / (1.0 + np.exp(-a)) * b
+
+
+def token_swiglu(x, idx, gate, w1, w3, w2):
+    """y[t] = sum over valid slots of gate * W2[e] h(x[t]); weights as fp64 values"""
+    y = np.zeros((x.shape[0], w2.shape[1]))
+    for t in range(x.shape[0]):
+        for j in range(idx.shape[1]):
+            e = int(idx[t, j])
+            if 0 <= e < w1.shape[0]:
+                y[t] += gate[t, j] * (swiglu_hidden(x[t:t + 1], w1[e], w3[e])[2] @ w2[e].T)[0]
+    return y

@@ -19,6 +19,9 @@ LIB_PATH = os.path.join(_PKG, "libmoe.so")
 
 MOE_F32 = 0
 MOE_BF16 = 1
+MOE_MX_E4M3 = 0
+MOE_MX_E2M1 = 1
+MOE_TOKEN_MAX_SLOTS = 1024
 
 STATUS_NAMES = {
     0: "MOE_OK",
@@ -43,7 +46,9 @@ EXPORTED = (
     "moe_gate_folded_supported", "moe_dgate_parts", "moe_permute_gates",
     "moe_expert_up_folded", "moe_expert_dgrad_down_folded", "moe_dgate_from_parts",
     "moe_expert_wgrad_folded", "moe_route_bwd_folded", "moe_route_noalloc",
-    "moe_route_noalloc_max_bytes",
+    "moe_route_noalloc_max_bytes", "moe_mx_scale_cols", "moe_mx_quantize", "moe_mx_dequantize",
+    "moe_rmsnorm", "moe_rmsnorm_bwd", "moe_rmsnorm_bwd_workspace_bytes", "moe_expert_up_mx",
+    "moe_expert_down_mx", "moe_token_swiglu", "moe_token_swiglu_workspace_bytes",
 )
 
 
@@ -120,6 +125,16 @@ _SIGNATURES = {
     "moe_route_flips": (_I32, [_I64, _I32, _I32, _P, _P, _P, _P, _P]),
     "moe_shuffle_plan": (_I32, [_I64, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _SZ,
                                 _P]),
+    "moe_mx_scale_cols": (_I32, [_I32]),
+    "moe_mx_quantize": (_I32, [_I64, _I32, _I32, _P, _I32, _P, _P, _P]),
+    "moe_mx_dequantize": (_I32, [_I64, _I32, _I32, _P, _P, _I32, _P, _P]),
+    "moe_rmsnorm": (_I32, [_DIMS, _P, _P, _P, _F32, _P, _P, _P, _P, _P, _P]),
+    "moe_rmsnorm_bwd": (_I32, [_DIMS, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_rmsnorm_bwd_workspace_bytes": (_SZ, [_DIMS]),
+    "moe_expert_up_mx": (_I32, [_DIMS, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_expert_down_mx": (_I32, [_DIMS, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_token_swiglu": (_I32, [_DIMS, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_token_swiglu_workspace_bytes": (_SZ, [_DIMS]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -633,3 +648,170 @@ def moe_route_flips(T, k, E, topk_idx_a, topk_idx_b, flips, n_flips, stream=None
                                _ptr(flips, "flips", torch.int32),
                                _ptr(n_flips, "n_flips", torch.int32), _stream(stream))
     _check(st, "moe_route_flips")
+
+
+# ---------------------------------------------------------------- the norm and the experts in low precision
+# These calls check shapes too, and run on the device of their tensors (which
+# need not be the current one), on that device's current stream unless one is
+# given.
+_BYTES = (torch.uint8, torch.float8_e4m3fn, torch.float8_e8m0fnu)
+_FORMATS = {"e4m3": (MOE_MX_E4M3, 1), "e2m1": (MOE_MX_E2M1, 2)}   # code, elements to a byte
+
+
+def _arg(t, name, dtypes, numel, device):
+    """Pointer of a contiguous tensor of `numel` values on `device`; None stays NULL."""
+    if t is None:
+        return None
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, is on {t.device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.numel() != numel:
+        raise ValueError(f"{name} must hold {numel} values, has shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _device_of(t, name):
+    if t is None or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t.device
+
+
+def _workspace(t, device):
+    """(pointer, bytes) of a workspace tensor; None is no workspace."""
+    if t is None:
+        return None, 0
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _enqueue(func, device, stream, *args):
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    fn = getattr(lib(), func)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, stream.cuda_stream)
+    _check(st, func)
+
+
+def moe_mx_scale_cols(cols) -> int:
+    """Bytes of a scale row of `cols` values (0 unless a positive multiple of 64)."""
+    return int(lib().moe_mx_scale_cols(int(cols)))
+
+
+def _mx_rows(t, name, q, scale, fmt):
+    """Checks shared by the two directions: (rows, cols, dtype code, format code, pointers)."""
+    if fmt not in _FORMATS:
+        raise ValueError(f"format must be 'e4m3' or 'e2m1', got {fmt!r}")
+    code, per_byte = _FORMATS[fmt]
+    device = _device_of(t, name)
+    if t.dim() == 0:
+        raise ValueError(f"{name} must have rows")
+    cols = t.shape[-1]
+    rows = t.numel() // cols if cols else 0
+    ptr = _arg(t, name, (torch.float32, torch.bfloat16), t.numel(), device)
+    dtype = MOE_BF16 if t.dtype == torch.bfloat16 else MOE_F32
+    scale_cols = moe_mx_scale_cols(cols)
+    qp, sp = q, scale
+    if scale_cols:   # else the library says what is wrong with cols
+        qp = _arg(q, "q", _BYTES, rows * cols // per_byte, device)
+        sp = _arg(scale, "scale", _BYTES, rows * scale_cols, device)
+    else:
+        qp = sp = None
+    return device, rows, cols, dtype, code, ptr, qp, sp
+
+
+def moe_mx_quantize(src, fmt, q, scale, stream=None):
+    """src [..., cols] fp32 or bf16 to elements q ("e4m3": a byte each, "e2m1": two
+    to a byte) and scale bytes [rows, moe_mx_scale_cols(cols)]."""
+    device, rows, cols, dtype, code, ptr, qp, sp = _mx_rows(src, "src", q, scale, fmt)
+    _enqueue("moe_mx_quantize", device, stream, rows, cols, dtype, ptr, code, qp, sp)
+
+
+def moe_mx_dequantize(q, scale, fmt, dst, stream=None):
+    """The values of q and scale into dst [..., cols] fp32 or bf16."""
+    device, rows, cols, dtype, code, ptr, qp, sp = _mx_rows(dst, "dst", q, scale, fmt)
+    _enqueue("moe_mx_dequantize", device, stream, rows, cols, code, qp, sp, dtype, ptr)
+
+
+def moe_rmsnorm(dims, x, residual, weight, eps, sum_out, y, q, q_scale, rstd, stream=None):
+    device = _device_of(x, "x")
+    act, T, d = (act_dtype(dims),), dims.T, dims.d
+    f32 = (torch.float32,)
+    _enqueue("moe_rmsnorm", device, stream, ctypes.byref(dims),
+             _arg(x, "x", act, T * d, device), _arg(residual, "residual", act, T * d, device),
+             _arg(weight, "weight", f32, d, device), float(eps),
+             _arg(sum_out, "sum", act, T * d, device), _arg(y, "y", act, T * d, device),
+             _arg(q, "q", _BYTES, T * d, device),
+             _arg(q_scale, "q_scale", _BYTES, T * moe_mx_scale_cols(d), device),
+             _arg(rstd, "rstd", f32, T, device))
+
+
+def moe_rmsnorm_bwd_workspace_bytes(dims) -> int:
+    return int(lib().moe_rmsnorm_bwd_workspace_bytes(ctypes.byref(dims)))
+
+
+def moe_rmsnorm_bwd(dims, dy, s, weight, rstd, dsum, dx, dweight, workspace, stream=None):
+    device = _device_of(dy, "dy")
+    act, T, d = (act_dtype(dims),), dims.T, dims.d
+    f32 = (torch.float32,)
+    _enqueue("moe_rmsnorm_bwd", device, stream, ctypes.byref(dims),
+             _arg(dy, "dy", act, T * d, device), _arg(s, "s", act, T * d, device),
+             _arg(weight, "weight", f32, d, device), _arg(rstd, "rstd", f32, T, device),
+             _arg(dsum, "dsum", act, T * d, device), _arg(dx, "dx", act, T * d, device),
+             _arg(dweight, "dweight", f32, d, device), *_workspace(workspace, device))
+
+
+def _mx_weight(w, w_scale, name, E, n, width, device):
+    return (_arg(w, name, (torch.uint8,), E * n * width // 2, device),
+            _arg(w_scale, name + "_scale", _BYTES, E * n * moe_mx_scale_cols(width), device))
+
+
+def moe_expert_up_mx(dims, xq, x_scale, src_token, expert_offsets, w1, w1_scale, w3, w3_scale,
+                     hq, h_scale, stream=None):
+    device = _device_of(xq, "xq")
+    T, d, E, f, R = dims.T, dims.d, dims.E, dims.f, dims.T * dims.k
+    i32, rows = (torch.int32,), R if src_token is None else T
+    _enqueue("moe_expert_up_mx", device, stream, ctypes.byref(dims),
+             _arg(xq, "xq", _BYTES, rows * d, device),
+             _arg(x_scale, "x_scale", _BYTES, rows * moe_mx_scale_cols(d), device),
+             _arg(src_token, "src_token", i32, R, device),
+             _arg(expert_offsets, "expert_offsets", i32, E + 1, device),
+             *_mx_weight(w1, w1_scale, "w1", E, f, d, device),
+             *_mx_weight(w3, w3_scale, "w3", E, f, d, device),
+             _arg(hq, "hq", _BYTES, R * f, device),
+             _arg(h_scale, "h_scale", _BYTES, R * moe_mx_scale_cols(f), device))
+
+
+def moe_expert_down_mx(dims, hq, h_scale, expert_offsets, w2, w2_scale, y_perm, stream=None):
+    device = _device_of(hq, "hq")
+    d, E, f, R = dims.d, dims.E, dims.f, dims.T * dims.k
+    _enqueue("moe_expert_down_mx", device, stream, ctypes.byref(dims),
+             _arg(hq, "hq", _BYTES, R * f, device),
+             _arg(h_scale, "h_scale", _BYTES, R * moe_mx_scale_cols(f), device),
+             _arg(expert_offsets, "expert_offsets", (torch.int32,), E + 1, device),
+             *_mx_weight(w2, w2_scale, "w2", E, d, f, device),
+             _arg(y_perm, "y_perm", (act_dtype(dims),), R * d, device))
+
+
+def moe_token_swiglu_workspace_bytes(dims) -> int:
+    return int(lib().moe_token_swiglu_workspace_bytes(ctypes.byref(dims)))
+
+
+def moe_token_swiglu(dims, x, topk_idx, topk_gate, w1, w1_scale, w3, w3_scale, w2, w2_scale, y,
+                     workspace, stream=None):
+    device = _device_of(x, "x")
+    act, T, d, E, f, R = (act_dtype(dims),), dims.T, dims.d, dims.E, dims.f, dims.T * dims.k
+    _enqueue("moe_token_swiglu", device, stream, ctypes.byref(dims),
+             _arg(x, "x", act, T * d, device), _arg(topk_idx, "topk_idx", (torch.int32,), R, device),
+             _arg(topk_gate, "topk_gate", (torch.float32,), R, device),
+             *_mx_weight(w1, w1_scale, "w1", E, f, d, device),
+             *_mx_weight(w3, w3_scale, "w3", E, f, d, device),
+             *_mx_weight(w2, w2_scale, "w2", E, d, f, device),
+             _arg(y, "y", act, T * d, device), *_workspace(workspace, device))

@@ -253,4 +253,36 @@ hipError_t launch_ep_pack(const moe_dims& dm, int32_t G, const void* x,
 hipError_t launch_ep_expand(const moe_dims& dm, const void* recv, const int32_t* assign_row,
                             const int32_t* pos, void* x_perm, hipStream_t s);
 
+// block-scaled rows (mx.hip)
+hipError_t launch_mx_quantize(int64_t rows, int32_t cols, int32_t act, const void* src,
+                              int32_t fmt, void* q, uint8_t* scale, hipStream_t s);
+hipError_t launch_mx_dequantize(int64_t rows, int32_t cols, int32_t act, const void* q,
+                                const uint8_t* scale, int32_t fmt, void* dst, hipStream_t s);
+
+// the norm before the layer
+hipError_t launch_rmsnorm(const moe_dims& dm, const void* x, const void* res, const float* weight,
+                          float eps, void* sum, void* y, void* q, uint8_t* q_scale, float* rstd,
+                          hipStream_t s);
+int rmsnorm_bwd_parts(const moe_dims& dm);   // weight-gradient partial sums (workspace: parts d floats)
+hipError_t launch_rmsnorm_bwd(const moe_dims& dm, const void* dy, const void* s_in,
+                              const float* weight, const float* rstd, const void* dsum, void* dx,
+                              float* dweight, float* ws_part, hipStream_t s);
+
+// low-precision experts: prompts (gemm_mx.hip) and a few tokens (token.hip)
+bool mx_tiles_ok(const moe_dims& dm);   // the grids stay below the launch limit
+hipError_t launch_up_mx(const moe_dims& dm, const void* xq, const uint8_t* x_scale,
+                        const int32_t* x_rows, const int32_t* offsets, const void* w1,
+                        const uint8_t* w1_scale, const void* w3, const uint8_t* w3_scale, void* hq,
+                        uint8_t* h_scale, hipStream_t s);
+hipError_t launch_down_mx(const moe_dims& dm, const void* hq, const uint8_t* h_scale,
+                          const int32_t* offsets, const void* w2, const uint8_t* w2_scale, void* y,
+                          hipStream_t s);
+size_t token_h_elems(const moe_dims& dm);
+size_t token_row_elems(const moe_dims& dm);
+hipError_t launch_token_swiglu(const moe_dims& dm, const void* x, const int32_t* idx,
+                               const float* gate, const void* w1, const uint8_t* w1_scale,
+                               const void* w3, const uint8_t* w3_scale, const void* w2,
+                               const uint8_t* w2_scale, void* y, bf16_t* ws_h, float* ws_rows,
+                               hipStream_t s);
+
 }  // namespace moe

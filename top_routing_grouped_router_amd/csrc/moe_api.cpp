@@ -245,6 +245,24 @@ PlanWs plan_ws(int64_t T, int32_t G, void* ws) {
   return r;
 }
 
+size_t rmsnorm_bwd_ws_bytes(const moe_dims& dm) {
+  return moe::align256(static_cast<size_t>(moe::rmsnorm_bwd_parts(dm)) * dm.d * sizeof(float));
+}
+
+struct TokenWs {
+  moe::bf16_t* h;
+  float* rows;
+  size_t bytes;
+};
+TokenWs token_ws(const moe_dims& dm, void* ws) {
+  Carver c;
+  TokenWs r;
+  r.h = c.take<moe::bf16_t>(ws, moe::token_h_elems(dm));
+  r.rows = c.take<float>(ws, moe::token_row_elems(dm));
+  r.bytes = c.off;
+  return r;
+}
+
 size_t workspace_needed(const moe_dims& dm, int32_t n_groups) {
   const int32_t G = std::max(n_groups, 1);
   size_t need = route_ws(dm, 1, nullptr).bytes;  // tile 1 is the largest layout
@@ -256,6 +274,7 @@ size_t workspace_needed(const moe_dims& dm, int32_t n_groups) {
   need = std::max(need, variant_ws(dm, G, nullptr).bytes);
   need = std::max(need, moe::align256(static_cast<size_t>(dm.E) * std::max(G, 64) * 4));
   need = std::max(need, plan_ws(dm.T, std::max(G, 64), nullptr).bytes);
+  need = std::max(need, rmsnorm_bwd_ws_bytes(dm));
   return need;
 }
 
@@ -296,6 +315,49 @@ moe_status check_gather(const moe_dims& dm, const void* x, const int32_t* src_to
     return fail(MOE_ERR_INVALID_ARGUMENT, "%s: 'src_token' is NULL", fn);
   if (dm.act == MOE_BF16 && dm.T * dm.d * 2 >= (int64_t(1) << 31))
     return fail(MOE_ERR_UNSUPPORTED, "%s: X must be under 2 GiB to be gathered", fn);
+  return MOE_OK;
+}
+
+// widths that the low-precision kernels' 32-bit offsets within a tile cover
+moe_status check_mx_dims(const moe_dims* dims, const char* fn) {
+  const moe_status st = check_dims(dims, fn);
+  if (st != MOE_OK) return st;
+  if (dims->d > (1 << 20) || dims->f > (1 << 20))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: d=%d and f=%d must be at most 2^20", fn, dims->d, dims->f);
+  return MOE_OK;
+}
+
+moe_status check_expert_mx(const moe_dims* dims, const char* fn) {
+  const moe_status st = check_mx_dims(dims, fn);
+  if (st != MOE_OK) return st;
+  if (!moe::mx_tiles_ok(*dims))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: T*k=%lld rows make too many tiles for one launch", fn,
+                static_cast<long long>(dims->T * dims->k));
+  return MOE_OK;
+}
+
+moe_status check_token(const moe_dims* dims, const char* fn) {
+  const moe_status st = check_mx_dims(dims, fn);
+  if (st != MOE_OK) return st;
+  if (dims->T * dims->k > MOE_TOKEN_MAX_SLOTS)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: T*k=%lld must be <= %d (moe_expert_up_mx takes more)", fn,
+                static_cast<long long>(dims->T * dims->k), MOE_TOKEN_MAX_SLOTS);
+  return MOE_OK;
+}
+
+moe_status check_mx_rows(int64_t rows, int32_t cols, int32_t dtype, int32_t format,
+                         const char* fn) {
+  if (rows < 0 || cols <= 0)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "%s: need rows >= 0 and cols > 0 (rows=%lld cols=%d)", fn,
+                static_cast<long long>(rows), cols);
+  if (cols % 64) return fail(MOE_ERR_UNSUPPORTED, "%s: cols=%d must be a multiple of 64", fn, cols);
+  if (rows > (int64_t(1) << 36) / cols)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: rows*cols must be at most 2^36", fn);
+  if (dtype != MOE_F32 && dtype != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: dtype=%d is neither MOE_F32 nor MOE_BF16", fn, dtype);
+  if (format != MOE_MX_E4M3 && format != MOE_MX_E2M1)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: format=%d is neither MOE_MX_E4M3 nor MOE_MX_E2M1", fn,
+                format);
   return MOE_OK;
 }
 
@@ -1291,6 +1353,161 @@ moe_status moe_route_bwd_folded(const moe_dims* dims, const void* x, const float
                                           w.dl_perm, w.dl_sel, w.partial,
                                           static_cast<hipStream_t>(stream), dgate_part,
                                           moe::dgate_parts_bf16(dm), dgate),
+                    __func__);
+}
+
+int32_t moe_mx_scale_cols(int32_t cols) {
+  return cols > 0 && cols % 64 == 0 ? (cols - 1) / 128 * 4 + 4 : 0;
+}
+
+moe_status moe_mx_quantize(int64_t rows, int32_t cols, int32_t src_dtype, const void* src,
+                           int32_t format, void* q, uint8_t* scale, void* stream) {
+  const moe_status st = check_mx_rows(rows, cols, src_dtype, format, __func__);
+  if (st != MOE_OK) return st;
+  MOE_REQUIRE_PTR(src, rows);
+  MOE_REQUIRE_PTR(q, rows);
+  MOE_REQUIRE_PTR(scale, rows);
+  return hip_status(moe::launch_mx_quantize(rows, cols, src_dtype, src, format, q, scale,
+                                            static_cast<hipStream_t>(stream)),
+                    __func__);
+}
+
+moe_status moe_mx_dequantize(int64_t rows, int32_t cols, int32_t format, const void* q,
+                             const uint8_t* scale, int32_t dst_dtype, void* dst, void* stream) {
+  const moe_status st = check_mx_rows(rows, cols, dst_dtype, format, __func__);
+  if (st != MOE_OK) return st;
+  MOE_REQUIRE_PTR(q, rows);
+  MOE_REQUIRE_PTR(scale, rows);
+  MOE_REQUIRE_PTR(dst, rows);
+  return hip_status(moe::launch_mx_dequantize(rows, cols, dst_dtype, q, scale, format, dst,
+                                              static_cast<hipStream_t>(stream)),
+                    __func__);
+}
+
+moe_status moe_rmsnorm(const moe_dims* dims, const void* x, const void* residual,
+                       const float* weight, float eps, void* sum, void* y, void* q,
+                       uint8_t* q_scale, float* rstd, void* stream) {
+  const moe_status st = check_dims(dims, __func__);
+  if (st != MOE_OK) return st;
+  const moe_dims& dm = *dims;
+  if (!(eps >= 0.0f) || std::isinf(eps))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "%s: eps=%g must be finite and >= 0", __func__, eps);
+  MOE_REQUIRE_PTR(x, dm.T);
+  MOE_OPTIONAL_PTR(residual);
+  MOE_REQUIRE_PTR(weight, dm.d);
+  MOE_OPTIONAL_PTR(sum);
+  MOE_OPTIONAL_PTR(y);
+  MOE_OPTIONAL_PTR(q);
+  MOE_OPTIONAL_PTR(q_scale);
+  MOE_OPTIONAL_PTR(rstd);
+  if (dm.T > 0 && !y && !q)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "%s: 'y' or 'q' has to be given", __func__);
+  if (dm.T > 0 && !q != !q_scale)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "%s: 'q' and 'q_scale' go together", __func__);
+  if (sum && sum == y)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "%s: 'sum' and 'y' are one tensor", __func__);
+  return hip_status(moe::launch_rmsnorm(dm, x, residual, weight, eps, sum, y, q, q_scale, rstd,
+                                        static_cast<hipStream_t>(stream)),
+                    __func__);
+}
+
+size_t moe_rmsnorm_bwd_workspace_bytes(const moe_dims* dims) {
+  if (check_dims(dims, __func__) != MOE_OK) return 0;
+  return rmsnorm_bwd_ws_bytes(*dims);
+}
+
+moe_status moe_rmsnorm_bwd(const moe_dims* dims, const void* dy, const void* s,
+                           const float* weight, const float* rstd, const void* dsum, void* dx,
+                           float* dweight, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  moe_status st = check_dims(dims, __func__);
+  if (st != MOE_OK) return st;
+  const moe_dims& dm = *dims;
+  MOE_REQUIRE_PTR(dy, dm.T);
+  MOE_REQUIRE_PTR(s, dm.T);
+  MOE_REQUIRE_PTR(weight, dm.d);
+  MOE_REQUIRE_PTR(rstd, dm.T);
+  MOE_OPTIONAL_PTR(dsum);
+  MOE_REQUIRE_PTR(dx, dm.T);
+  MOE_REQUIRE_PTR(dweight, dm.d);
+  st = check_ws(workspace, workspace_bytes, rmsnorm_bwd_ws_bytes(dm), __func__);
+  if (st != MOE_OK) return st;
+  return hip_status(moe::launch_rmsnorm_bwd(dm, dy, s, weight, rstd, dsum, dx, dweight,
+                                            static_cast<float*>(workspace),
+                                            static_cast<hipStream_t>(stream)),
+                    __func__);
+}
+
+moe_status moe_expert_up_mx(const moe_dims* dims, const void* xq, const uint8_t* x_scale,
+                            const int32_t* src_token, const int32_t* expert_offsets,
+                            const void* w1, const uint8_t* w1_scale, const void* w3,
+                            const uint8_t* w3_scale, void* hq, uint8_t* h_scale, void* stream) {
+  const moe_status st = check_expert_mx(dims, __func__);
+  if (st != MOE_OK) return st;
+  const moe_dims& dm = *dims;
+  MOE_REQUIRE_PTR(xq, dm.T);
+  MOE_REQUIRE_PTR(x_scale, dm.T);
+  MOE_OPTIONAL_PTR(src_token);
+  if (src_token && dm.T * dm.d >= (int64_t(1) << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: X must be under 2 GiB to be gathered", __func__);
+  MOE_REQUIRE_PTR(expert_offsets, dm.E + 1);
+  MOE_REQUIRE_PTR(w1, dm.E);
+  MOE_REQUIRE_PTR(w1_scale, dm.E);
+  MOE_REQUIRE_PTR(w3, dm.E);
+  MOE_REQUIRE_PTR(w3_scale, dm.E);
+  MOE_REQUIRE_PTR(hq, dm.T);
+  MOE_REQUIRE_PTR(h_scale, dm.T);
+  return hip_status(moe::launch_up_mx(dm, xq, x_scale, src_token, expert_offsets, w1, w1_scale, w3,
+                                      w3_scale, hq, h_scale, static_cast<hipStream_t>(stream)),
+                    __func__);
+}
+
+moe_status moe_expert_down_mx(const moe_dims* dims, const void* hq, const uint8_t* h_scale,
+                              const int32_t* expert_offsets, const void* w2,
+                              const uint8_t* w2_scale, void* y_perm, void* stream) {
+  const moe_status st = check_expert_mx(dims, __func__);
+  if (st != MOE_OK) return st;
+  const moe_dims& dm = *dims;
+  MOE_REQUIRE_PTR(hq, dm.T);
+  MOE_REQUIRE_PTR(h_scale, dm.T);
+  MOE_REQUIRE_PTR(expert_offsets, dm.E + 1);
+  MOE_REQUIRE_PTR(w2, dm.E);
+  MOE_REQUIRE_PTR(w2_scale, dm.E);
+  MOE_REQUIRE_PTR(y_perm, dm.T);
+  return hip_status(moe::launch_down_mx(dm, hq, h_scale, expert_offsets, w2, w2_scale, y_perm,
+                                        static_cast<hipStream_t>(stream)),
+                    __func__);
+}
+
+size_t moe_token_swiglu_workspace_bytes(const moe_dims* dims) {
+  if (check_token(dims, __func__) != MOE_OK) return 0;
+  return token_ws(*dims, nullptr).bytes;
+}
+
+moe_status moe_token_swiglu(const moe_dims* dims, const void* x, const int32_t* topk_idx,
+                            const float* topk_gate, const void* w1, const uint8_t* w1_scale,
+                            const void* w3, const uint8_t* w3_scale, const void* w2,
+                            const uint8_t* w2_scale, void* y, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  moe_status st = check_token(dims, __func__);
+  if (st != MOE_OK) return st;
+  const moe_dims& dm = *dims;
+  MOE_REQUIRE_PTR(x, dm.T);
+  MOE_REQUIRE_PTR(topk_idx, dm.T);
+  MOE_REQUIRE_PTR(topk_gate, dm.T);
+  MOE_REQUIRE_PTR(w1, dm.E);
+  MOE_REQUIRE_PTR(w1_scale, dm.E);
+  MOE_REQUIRE_PTR(w3, dm.E);
+  MOE_REQUIRE_PTR(w3_scale, dm.E);
+  MOE_REQUIRE_PTR(w2, dm.E);
+  MOE_REQUIRE_PTR(w2_scale, dm.E);
+  MOE_REQUIRE_PTR(y, dm.T);
+  st = check_ws(workspace, workspace_bytes, token_ws(dm, nullptr).bytes, __func__);
+  if (st != MOE_OK) return st;
+  const TokenWs w = token_ws(dm, workspace);
+  return hip_status(moe::launch_token_swiglu(dm, x, topk_idx, topk_gate, w1, w1_scale, w3, w3_scale,
+                                             w2, w2_scale, y, w.h, w.rows,
+                                             static_cast<hipStream_t>(stream)),
                     __func__);
 }
 

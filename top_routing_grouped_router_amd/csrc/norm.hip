@@ -1,0 +1,503 @@
+// The root-mean-square norm in front of the layer, with the residual's addition
+// and 8-bit rows for low-precision experts, and its backward pass.
+//
+//   s = round(x + r);  rstd = 1 / sqrt(mean(s^2) + eps);  y = (s rstd) w
+// The norm is taken of s as it is stored (rounded to the act type), so the
+// backward pass, which reads s, differentiates what the forward computed.
+// Squares, means and products are fp32; y is rounded once, and the 8-bit rows
+// come from the fp32 y, not from its rounding.
+//   n = s rstd;  g = dy w;  dx = rstd (g - n mean(g n)) + dsum;  dw = sum_t dy n
+//
+// Every pass is bound by HBM: each tensor is read and written once, with the
+// row held in registers between the sum of squares and the scaling.  A row
+// belongs to one wavefront where it fits its registers and there are rows
+// enough to fill the GPU (no barrier, no LDS), else to a workgroup of four
+// (fewer bytes per lane: a few rows are bound by latency, not bytes).  Rows
+// longer than a workgroup's registers are read twice.
+#include <algorithm>
+
+#include "mx.h"
+
+namespace moe {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// sum over the W wavefronts of a row (W = 1: the wavefront's own), the same in
+// every lane.  The caller's loop may come here again at once: two barriers.
+template <int W>
+__device__ __forceinline__ float row_sum(float v) {
+  v = wave_sum(v);
+  if constexpr (W > 1) {
+    __shared__ float part[W];
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = part[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += part[w];
+    __syncthreads();
+  }
+  return v;
+}
+
+// sum of N squares by halves: the error of a long row's sum, which shifts every
+// 8-bit rounding of the row, grows with the depth of the tree
+template <int N>
+__device__ __forceinline__ float squares(const float* v) {
+  if constexpr (N == 1) return v[0] * v[0];
+  else return squares<N / 2>(v) + squares<N / 2>(v + N / 2);
+}
+
+struct NormArgs {
+  const void* x;
+  const void* res;
+  const float* weight;
+  void* sum;
+  void* y;
+  uint8_t* q;
+  uint8_t* q_scale;
+  float* rstd;
+  int64_t T;
+  int d;
+  float eps;
+};
+
+__device__ __forceinline__ uint4 load16(const void* p, int64_t piece) {
+  return reinterpret_cast<const uint4*>(p)[piece];
+}
+
+// s of one 16-byte piece, as stored, in fp32; writes it to `sum` if there is one
+template <typename T>
+__device__ __forceinline__ void piece_sum(const NormArgs& g, int64_t at, uint4 xv, uint4 rv,
+                                          float* s) {
+  constexpr int N = Act<T>::kPer16B;
+  unpack16(xv, s, T{});
+  if (g.res) {
+    float r[N];
+    unpack16(rv, r, T{});
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] += r[i];
+    const uint4 packed = pack16(s, T{});
+    if (g.sum) reinterpret_cast<uint4*>(g.sum)[at] = packed;
+    unpack16(packed, s, T{});
+  } else if (g.sum) {
+    reinterpret_cast<uint4*>(g.sum)[at] = xv;
+  }
+}
+
+// y of one piece from s: the act row, the 8-bit row and its scales
+template <typename T>
+__device__ __forceinline__ void piece_out(const NormArgs& g, int64_t row, int p, int per_row,
+                                          float rstd, const float* s) {
+  constexpr int N = Act<T>::kPer16B;
+  constexpr int kLanes = 32 / N;
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const float4 w = reinterpret_cast<const float4*>(g.weight)[p * (N / 4) + i];
+    v[4 * i] = s[4 * i] * rstd * w.x;
+    v[4 * i + 1] = s[4 * i + 1] * rstd * w.y;
+    v[4 * i + 2] = s[4 * i + 2] * rstd * w.z;
+    v[4 * i + 3] = s[4 * i + 3] * rstd * w.w;
+  }
+  if (g.y) reinterpret_cast<uint4*>(g.y)[row * per_row + p] = pack16(v, T{});
+  if (g.q) {
+    const uint32_t sb = mx_store<kE4M3, N>(v, g.q + (row * per_row + p) * N);
+    if (p % kLanes == 0) {
+      const int ld = mx_scale_ld(g.d), b = p / kLanes;
+      uint8_t* out = g.q_scale + row * ld + b;
+      *out = static_cast<uint8_t>(sb);
+      if (b == ld - 3 && g.d % 128) out[1] = out[2] = 0;   // the row's padding
+    }
+  }
+}
+
+// W wavefronts per row, NV 16-byte pieces per lane
+template <typename T, int W, int NV>
+__global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs g) {
+  constexpr int N = Act<T>::kPer16B;
+  constexpr int L = 64 * W;   // lanes of a row
+  constexpr int kRows = kThreads / L;
+  const int lane = threadIdx.x % L, per_row = g.d / N;
+  // one turn unless the grid limit is passed (whole wavefronts leave, and whole
+  // workgroups where they join)
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / L; row < g.T;
+       row += static_cast<int64_t>(gridDim.x) * kRows) {
+    uint4 xv[NV], rv[NV];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int p = lane + u * L;
+      xv[u] = rv[u] = make_uint4(0, 0, 0, 0);
+      if (p < per_row) {
+        xv[u] = load16(g.x, row * per_row + p);
+        if (g.res) rv[u] = load16(g.res, row * per_row + p);
+      }
+    }
+    float s[NV][N], ss = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int p = lane + u * L;
+      if (p < per_row) {
+        piece_sum<T>(g, row * per_row + p, xv[u], rv[u], s[u]);
+        ss += squares<N>(s[u]);
+      }
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<W>(ss) / static_cast<float>(g.d) + g.eps);
+    if (g.rstd && lane == 0) g.rstd[row] = rstd;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int p = lane + u * L;
+      if (p < per_row) piece_out<T>(g, row, p, per_row, rstd, s[u]);
+    }
+  }
+}
+
+// rows of any length, one workgroup each, read twice (the second time s comes
+// from `sum` where it was written, since `sum` may be x or the residual)
+template <typename T>
+__global__ __launch_bounds__(kThreads) void norm_long_kernel(NormArgs g) {
+  constexpr int N = Act<T>::kPer16B;
+  const int per_row = g.d / N;
+  NormArgs again = g;
+  again.sum = nullptr;
+  if (g.sum) {
+    again.x = g.sum;
+    again.res = nullptr;
+  }
+  for (int64_t row = blockIdx.x; row < g.T; row += gridDim.x) {
+    float ss = 0.0f;
+    for (int p = threadIdx.x; p < per_row; p += kThreads) {
+      float s[N];
+      const int64_t at = row * per_row + p;
+      piece_sum<T>(g, at, load16(g.x, at), g.res ? load16(g.res, at) : make_uint4(0, 0, 0, 0), s);
+      ss += squares<N>(s);
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<kWaves>(ss) / static_cast<float>(g.d) + g.eps);
+    if (g.rstd && threadIdx.x == 0) g.rstd[row] = rstd;
+    for (int p = threadIdx.x; p < per_row; p += kThreads) {
+      float s[N];
+      const int64_t at = row * per_row + p;
+      piece_sum<T>(again, at, load16(again.x, at),
+                   again.res ? load16(again.res, at) : make_uint4(0, 0, 0, 0), s);
+      piece_out<T>(g, row, p, per_row, rstd, s);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- backward
+
+struct NormBwdArgs {
+  const void* dy;
+  const void* s;
+  const float* weight;
+  const float* rstd;
+  const void* dsum;
+  void* dx;
+  float* part;     // [workgroups, d] weight-gradient partial sums
+  int64_t T;
+  int64_t chunk;   // rows of a workgroup
+  int d;
+};
+
+// dx of one piece
+template <typename T>
+__device__ __forceinline__ void dx_out(const NormBwdArgs& a, int64_t at, float rstd, float c,
+                                       const float* gw, const float* n, uint4 dsv) {
+  constexpr int N = Act<T>::kPer16B;
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = rstd * (gw[i] - n[i] * c);
+  if (a.dsum) {
+    float t[N];
+    unpack16(dsv, t, T{});
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += t[i];
+  }
+  reinterpret_cast<uint4*>(a.dx)[at] = pack16(v, T{});
+}
+
+// A workgroup takes `chunk` consecutive rows, W wavefronts to a row, and keeps
+// the weight gradient of its lanes' columns in registers over all of them; the
+// 4 / W row streams are then added in a fixed order.
+template <typename T, int W, int NV>
+__global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormBwdArgs a) {
+  constexpr int N = Act<T>::kPer16B;
+  constexpr int L = 64 * W, S = kThreads / L;
+  const int stream = threadIdx.x / L, lane = threadIdx.x % L, per_row = a.d / N;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
+  const int64_t r1 = min(r0 + a.chunk, a.T);
+  float w[NV][N], dw[NV][N];
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int p = lane + u * L;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      dw[u][i] = 0.0f;
+      w[u][i] = p < per_row ? a.weight[p * N + i] : 0.0f;
+    }
+  }
+  for (int64_t row = r0 + stream; row < r1; row += S) {
+    uint4 dyv[NV], sv[NV], dsv[NV];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int p = lane + u * L;
+      dyv[u] = sv[u] = dsv[u] = make_uint4(0, 0, 0, 0);
+      if (p < per_row) {
+        dyv[u] = load16(a.dy, row * per_row + p);
+        sv[u] = load16(a.s, row * per_row + p);
+        if (a.dsum) dsv[u] = load16(a.dsum, row * per_row + p);
+      }
+    }
+    const float rstd = a.rstd[row];
+    float dot = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      float dy[N], s[N];
+      unpack16(dyv[u], dy, T{});
+      unpack16(sv[u], s, T{});
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float n = s[i] * rstd;
+        dot += dy[i] * w[u][i] * n;
+        dw[u][i] += dy[i] * n;
+      }
+    }
+    const float c = row_sum<W>(dot) / static_cast<float>(a.d);
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int p = lane + u * L;
+      if (p >= per_row) continue;
+      float gw[N], n[N];
+      unpack16(dyv[u], gw, T{});
+      unpack16(sv[u], n, T{});
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        gw[i] *= w[u][i];
+        n[i] *= rstd;
+      }
+      dx_out<T>(a, row * per_row + p, rstd, c, gw, n, dsv[u]);
+    }
+  }
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * a.d;
+  __shared__ float lds[S > 1 ? L * NV * N : 1];
+  for (int t = 0; t < S; ++t) {
+    if (stream == t) {
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        const int p = lane + u * L;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          if (S > 1 && t > 0) dw[u][i] += lds[(u * N + i) * L + lane];
+          if (t + 1 < S) lds[(u * N + i) * L + lane] = dw[u][i];
+        }
+        if (t + 1 == S && p < per_row) {
+#pragma unroll
+          for (int i = 0; i < N; i += 4)
+            *reinterpret_cast<float4*>(part + p * N + i) =
+                make_float4(dw[u][i], dw[u][i + 1], dw[u][i + 2], dw[u][i + 3]);
+        }
+      }
+    }
+    if (t + 1 < S) __syncthreads();
+  }
+}
+
+// dx of rows of any length, one workgroup each, read twice
+template <typename T>
+__global__ __launch_bounds__(kThreads) void norm_bwd_long_kernel(NormBwdArgs a) {
+  constexpr int N = Act<T>::kPer16B;
+  const int per_row = a.d / N;
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+    const float rstd = a.rstd[row];
+    float c = 0.0f;
+    for (int turn = 0; turn < 2; ++turn) {
+      float dot = 0.0f;
+      for (int p = threadIdx.x; p < per_row; p += kThreads) {
+        const int64_t at = row * per_row + p;
+        float gw[N], n[N];
+        unpack16(load16(a.dy, at), gw, T{});
+        unpack16(load16(a.s, at), n, T{});
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          gw[i] *= a.weight[p * N + i];
+          n[i] *= rstd;
+          dot += gw[i] * n[i];
+        }
+        if (turn)
+          dx_out<T>(a, at, rstd, c, gw, n, a.dsum ? load16(a.dsum, at) : make_uint4(0, 0, 0, 0));
+      }
+      if (!turn) c = row_sum<kWaves>(dot) / static_cast<float>(a.d);
+    }
+  }
+}
+
+// the weight gradient's partial sums of long rows: one lane per 16-byte piece
+// of the row, over the workgroup's chunk of rows.  Runs before the dx kernel,
+// since dx may be written over dy.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void norm_dw_long_kernel(NormBwdArgs a) {
+  constexpr int N = Act<T>::kPer16B;
+  const int per_row = a.d / N, p = blockIdx.y * kThreads + threadIdx.x;
+  if (p >= per_row) return;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
+  const int64_t r1 = min(r0 + a.chunk, a.T);
+  float dw[N] = {};
+  for (int64_t row = r0; row < r1; ++row) {
+    const float rstd = a.rstd[row];
+    float dy[N], s[N];
+    unpack16(load16(a.dy, row * per_row + p), dy, T{});
+    unpack16(load16(a.s, row * per_row + p), s, T{});
+#pragma unroll
+    for (int i = 0; i < N; ++i) dw[i] += dy[i] * (s[i] * rstd);
+  }
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * a.d + p * N;
+#pragma unroll
+  for (int i = 0; i < N; ++i) part[i] = dw[i];
+}
+
+// dweight[c] = sum of the partial sums in workgroup order: 16 columns (four
+// lanes of float4) by 64 runs of partials per workgroup, then the runs in order
+__global__ __launch_bounds__(kThreads) void norm_dw_kernel(const float* part, int parts, int d,
+                                                           float* dweight) {
+  constexpr int kRuns = 64;
+  __shared__ float4 lds[kRuns][4];
+  const int c4 = threadIdx.x & 3, run = threadIdx.x >> 2;
+  const int col = blockIdx.x * 16 + c4 * 4;   // d is a multiple of 64
+  const int len = (parts + kRuns - 1) / kRuns;
+  const int b = run * len, e = min(b + len, parts);
+  float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+  for (int i = b; i < e; ++i) {
+    const float4 t = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(i) * d + col);
+    v.x += t.x;
+    v.y += t.y;
+    v.z += t.z;
+    v.w += t.w;
+  }
+  lds[run][c4] = v;
+  __syncthreads();
+  if (run == 0) {
+    for (int i = 1; i < kRuns; ++i) {
+      const float4 t = lds[i][c4];
+      v.x += t.x;
+      v.y += t.y;
+      v.z += t.z;
+      v.w += t.w;
+    }
+    *reinterpret_cast<float4*>(dweight + col) = v;
+  }
+}
+
+// Pieces per lane (a power of two) that hold a row of `pieces` 16-byte pieces
+// in `lanes` lanes; 0 if that is more than 8 (registers)
+int pieces_per_lane(int pieces, int lanes) {
+  for (int nv = 1; nv <= 8; nv *= 2)
+    if (pieces <= nv * lanes) return nv;
+  return 0;
+}
+
+// workgroups for `n` of rows: a launch holds fewer than 2^32 threads
+unsigned row_grid(int64_t n) { return static_cast<unsigned>(std::min<int64_t>(n, 1 << 23)); }
+
+// A wavefront per row from this many rows on (a wavefront for each of the 1024
+// SIMDs); below it the GPU is not full and a row's latency counts.
+constexpr int64_t kWaveRows = 1024;
+
+template <typename T, int W, int NV>
+hipError_t run_norm(const NormArgs& g, hipStream_t s) {
+  hipLaunchKernelGGL((norm_kernel<T, W, NV>), dim3(row_grid((g.T * W + kWaves - 1) / kWaves)),
+                     dim3(kThreads), 0, s, g);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t norm(const NormArgs& g, hipStream_t s) {
+  const int pieces = g.d / Act<T>::kPer16B;
+  const int one = pieces_per_lane(pieces, 64), four = pieces_per_lane(pieces, 256);
+  if (one && one <= 4 && (g.T >= kWaveRows || one == 1)) {
+    switch (one) {
+      case 1: return run_norm<T, 1, 1>(g, s);
+      case 2: return run_norm<T, 1, 2>(g, s);
+      default: return run_norm<T, 1, 4>(g, s);
+    }
+  }
+  switch (four) {
+    case 1: return run_norm<T, kWaves, 1>(g, s);
+    case 2: return run_norm<T, kWaves, 2>(g, s);
+    case 4: return run_norm<T, kWaves, 4>(g, s);
+    case 8: return run_norm<T, kWaves, 8>(g, s);
+  }
+  hipLaunchKernelGGL((norm_long_kernel<T>), dim3(row_grid(g.T)), dim3(kThreads), 0, s,
+                     g);
+  return hipGetLastError();
+}
+
+template <typename T, int W, int NV>
+hipError_t run_norm_bwd(const NormBwdArgs& a, int parts, hipStream_t s) {
+  hipLaunchKernelGGL((norm_bwd_kernel<T, W, NV>), dim3(parts), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t norm_bwd(const NormBwdArgs& a, int parts, hipStream_t s) {
+  const int pieces = a.d / Act<T>::kPer16B;
+  const int one = pieces_per_lane(pieces, 64), four = pieces_per_lane(pieces, 256);
+  if (one && one <= 4) {
+    switch (one) {
+      case 1: return run_norm_bwd<T, 1, 1>(a, parts, s);
+      case 2: return run_norm_bwd<T, 1, 2>(a, parts, s);
+      default: return run_norm_bwd<T, 1, 4>(a, parts, s);
+    }
+  }
+  switch (four) {   // rows of 4 or fewer pieces per lane; 2 is the least here
+    case 2: return run_norm_bwd<T, kWaves, 2>(a, parts, s);
+    case 4: return run_norm_bwd<T, kWaves, 4>(a, parts, s);
+  }
+  const unsigned cols = static_cast<unsigned>((pieces + kThreads - 1) / kThreads);
+  hipLaunchKernelGGL((norm_dw_long_kernel<T>), dim3(parts, cols), dim3(kThreads), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((norm_bwd_long_kernel<T>), dim3(row_grid(a.T)), dim3(kThreads),
+                     0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const moe_dims& dm, const void* x, const void* res, const float* weight,
+                          float eps, void* sum, void* y, void* q, uint8_t* q_scale, float* rstd,
+                          hipStream_t s) {
+  if (dm.T == 0) return hipSuccess;
+  NormArgs g{x, res, weight, sum, y, static_cast<uint8_t*>(q), q_scale, rstd, dm.T, dm.d, eps};
+  return dm.act == MOE_BF16 ? norm<bf16_t>(g, s) : norm<float>(g, s);
+}
+
+// Workgroups of the backward pass: two for each of the 256 CUs, at least 4 rows each
+int rmsnorm_bwd_parts(const moe_dims& dm) {
+  return static_cast<int>(std::min<int64_t>((dm.T + 3) / 4, 512));
+}
+
+hipError_t launch_rmsnorm_bwd(const moe_dims& dm, const void* dy, const void* s_in,
+                              const float* weight, const float* rstd, const void* dsum, void* dx,
+                              float* dweight, float* ws_part, hipStream_t s) {
+  const int parts = rmsnorm_bwd_parts(dm);
+  if (parts > 0) {
+    const NormBwdArgs a{dy, s_in, weight, rstd, dsum, dx, ws_part, dm.T,
+                        (dm.T + parts - 1) / parts, dm.d};
+    const hipError_t e =
+        dm.act == MOE_BF16 ? norm_bwd<bf16_t>(a, parts, s) : norm_bwd<float>(a, parts, s);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(norm_dw_kernel, dim3(dm.d / 16), dim3(kThreads), 0, s, ws_part, parts, dm.d,
+                     dweight);
+  return hipGetLastError();
+}
+
+}  // namespace moe
