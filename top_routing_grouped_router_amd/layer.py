@@ -32,6 +32,15 @@ keeps dW1, dW3, dW2 as the fp32 sums (not rounded to bf16), and
 recompute=True hands the backward no saved a, b, h, so that it recomputes
 them with the forward kernel (the forward still stores them here; the results
 are the same bits).  Neither combines with fold_gate.
+
+pre_norm=True puts the root-mean-square norm and the residual's addition in
+front (moe_rmsnorm, moe_rmsnorm_bwd): the layer reads norm(x + residual), and
+`stream` holds the sum that the block's output is added to, usually by the next
+block's norm.
+
+MoEServeLayer is the forward alone with the expert weights in 4 bits: norm,
+router, and then moe_token_swiglu for a few tokens or moe_permute ->
+moe_expert_up_mx -> moe_expert_down_mx -> moe_combine for more.
 """
 from __future__ import annotations
 
@@ -45,7 +54,7 @@ class MoELayer:
                  n_groups: int = 1, near_tie_eps: float = 1e-3, device="cuda",
                  gather: bool = False, capacity_factor=None, aux_coef: float = 0.0,
                  z_coef: float = 0.0, fold_gate: bool = False, wgrad_dtype=None,
-                 recompute: bool = False):
+                 recompute: bool = False, pre_norm: bool = False, norm_eps: float = 1e-6):
         self.dims = L.make_dims(T, d, E, f, k, act)
         self.wgrad_dtype = act if wgrad_dtype is None else wgrad_dtype
         self.recompute = bool(recompute)
@@ -116,6 +125,14 @@ class MoELayer:
             need = L.moe_grouped_swiglu_bwd_workspace_bytes(self.dims, True)
             if need > self.workspace.numel():
                 self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        self.pre_norm = bool(pre_norm)
+        self.norm_eps = float(norm_eps)
+        self.stream = None   # what was normed: the sum, or x without a residual
+        self.norm_sum = empty(T, d, **ea) if self.pre_norm else None
+        self.xn = empty(T, d, **ea) if self.pre_norm else None
+        self.rstd = empty(T, **e32) if self.pre_norm else None
+        self.dstream = empty(T, d, **ea) if self.pre_norm else None
+        self.dnorm = empty(d, **e32) if self.pre_norm else None
 
     # ------------------------------------------------------------------ forward
     def route(self, x, wr):
@@ -153,10 +170,25 @@ class MoELayer:
                                      self.a, self.b, self.h, self.y_perm)
         L.moe_combine(self.dims, self.y_perm, self.pos, self.topk_gate, self.y)
 
-    def forward(self, x, wr, w1, w3, w2, routing=None):
+    def norm(self, x, norm_weight, residual=None):
+        """The pre-norm alone: the layer's input, from x and the residual."""
+        if not self.pre_norm:
+            raise ValueError("the layer was made without pre_norm")
+        self.stream = x if residual is None else self.norm_sum
+        L.moe_rmsnorm(self.dims, x, residual, norm_weight, self.norm_eps,
+                      None if residual is None else self.norm_sum, self.xn, None, None, self.rstd)
+        return self.xn
+
+    def forward(self, x, wr, w1, w3, w2, routing=None, norm_weight=None, residual=None):
         """routing: optional (topk_idx, topk_gate) device tensors that replace the
         router's decision after it has run (used to compare the downstream
-        steps on a routing fixed from outside)."""
+        steps on a routing fixed from outside).
+        norm_weight [d] fp32 and residual [T,d] or None: with pre_norm only."""
+        if self.pre_norm != (norm_weight is not None) or (residual is not None
+                                                          and not self.pre_norm):
+            raise ValueError("norm_weight goes with pre_norm=True, and so does residual")
+        if self.pre_norm:
+            x = self.norm(x, norm_weight, residual)
         self.route(x, wr)
         if routing is not None:
             self.topk_idx.copy_(routing[0])
@@ -165,7 +197,23 @@ class MoELayer:
         return self.y
 
     # ------------------------------------------------------------------ backward
-    def backward(self, dy, x, wr, w1, w3, w2):
+    def backward(self, dy, x, wr, w1, w3, w2, norm_weight=None, dsum=None):
+        """The gradient of the forward's x.  With pre_norm that is dstream, the
+        gradient of x and of the residual alike (dx is the norm output's, dnorm
+        the norm weight's); dsum [T,d] or None is added to it: the gradient that
+        reaches `stream` from elsewhere."""
+        if self.pre_norm != (norm_weight is not None) or (dsum is not None and not self.pre_norm):
+            raise ValueError("norm_weight goes with pre_norm=True, and so does dsum")
+        if not self.pre_norm:
+            return self._layer_bwd(dy, x, wr, w1, w3, w2)
+        if self.stream is None:
+            raise ValueError("backward before forward")
+        self._layer_bwd(dy, self.xn, wr, w1, w3, w2)
+        L.moe_rmsnorm_bwd(self.dims, self.dx, self.stream, norm_weight, self.rstd, dsum,
+                          self.dstream, self.dnorm, self.workspace)
+        return self.dstream
+
+    def _layer_bwd(self, dy, x, wr, w1, w3, w2):
         if self.fold_gate:
             L.moe_expert_dgrad_down_folded(self.dims, dy, self.src_token, self.expert_offsets,
                                            self.gate_perm, w2, self.a, self.b, self.da, self.db,
@@ -216,6 +264,85 @@ class MoELayer:
                             self.dwr, self.workspace)
         return self.dx
 
-    def step(self, x, wr, w1, w3, w2, dy):
-        self.forward(x, wr, w1, w3, w2)
-        self.backward(dy, x, wr, w1, w3, w2)
+    def step(self, x, wr, w1, w3, w2, dy, norm_weight=None, residual=None, dsum=None):
+        self.forward(x, wr, w1, w3, w2, norm_weight=norm_weight, residual=residual)
+        self.backward(dy, x, wr, w1, w3, w2, norm_weight=norm_weight, dsum=dsum)
+
+
+class MoEServeLayer:
+    """The layer's forward with 4-bit expert weights, for up to max_tokens tokens.
+
+    Up to few_slots token-expert pairs go through moe_token_swiglu (activations
+    in `act`, nothing sorted), more through the grouped products on 8-bit rows.
+    The outputs are buffers that the next forward overwrites.
+    """
+
+    def __init__(self, max_tokens: int, d: int, E: int, f: int, k: int, act: torch.dtype,
+                 norm_eps: float = 1e-6, few_slots: int = 256, device="cuda"):
+        self.T, self.d, self.E, self.f, self.k, self.act = max_tokens, d, E, f, k, act
+        self.norm_eps = float(norm_eps)
+        self.few_slots = min(int(few_slots), L.MOE_TOKEN_MAX_SLOTS)
+        dev = torch.device(device)
+        T, R = max(max_tokens, 1), max(max_tokens * k, 1)
+
+        def empty(*shape, dtype):
+            return torch.empty(*shape, dtype=dtype, device=dev)
+
+        f32, i32, u8 = torch.float32, torch.int32, torch.uint8
+        ld, lf = L.moe_mx_scale_cols(d), L.moe_mx_scale_cols(f)
+        self.w1, self.w1_scale = empty(E, f, d // 2, dtype=u8), empty(E, f, ld, dtype=u8)
+        self.w3, self.w3_scale = empty(E, f, d // 2, dtype=u8), empty(E, f, ld, dtype=u8)
+        self.w2, self.w2_scale = empty(E, d, f // 2, dtype=u8), empty(E, d, lf, dtype=u8)
+        self.norm_sum, self.xn, self.y = (empty(T, d, dtype=act) for _ in range(3))
+        self.xq, self.x_scale = empty(T, d, dtype=u8), empty(T, ld, dtype=u8)
+        self.hq, self.h_scale = empty(R, f, dtype=u8), empty(R, lf, dtype=u8)
+        self.y_perm = empty(R, d, dtype=act)
+        self.logits, self.margin = empty(T, E, dtype=f32), empty(T, dtype=f32)
+        self.topk_idx, self.topk_gate = empty(T, k, dtype=i32), empty(T, k, dtype=f32)
+        self.near_tie_count = empty(1, dtype=i32)
+        self.counts, self.offsets = empty(E, dtype=i32), empty(E + 1, dtype=i32)
+        self.pos, self.src_token = empty(T, k, dtype=i32), empty(R, dtype=i32)
+        few = self._dims(min(max_tokens, self.few_slots // k))
+        need = max(L.workspace_bytes(self._dims(max_tokens)),
+                   L.moe_token_swiglu_workspace_bytes(few), 256)
+        self.workspace = empty(need, dtype=u8)
+
+    def _dims(self, T):
+        return L.make_dims(T, self.d, self.E, self.f, self.k, self.act)
+
+    def load(self, w1, w3, w2):
+        """Quantises the expert weights, [E,f,d], [E,f,d] and [E,d,f] in fp32 or bf16."""
+        for w, name, shape in ((w1, "w1", (self.E, self.f, self.d)),
+                               (w3, "w3", (self.E, self.f, self.d)),
+                               (w2, "w2", (self.E, self.d, self.f))):
+            if tuple(w.shape) != shape:
+                raise ValueError(f"{name} must be {shape}, is {tuple(w.shape)}")
+            L.moe_mx_quantize(w, "e2m1", getattr(self, name), getattr(self, name + "_scale"))
+
+    def forward(self, x, norm_weight, wr, residual=None):
+        """x [T,d], T <= max_tokens: (y, stream), the experts' sum for norm(x +
+        residual) and x + residual (x itself without one)."""
+        T = x.shape[0]
+        if x.dim() != 2 or x.shape[1] != self.d or T > self.T:
+            raise ValueError(f"x must be [T, {self.d}] with T <= {self.T}, is {tuple(x.shape)}")
+        R = T * self.k
+        dims, few = self._dims(T), R <= self.few_slots
+        stream = x if residual is None else self.norm_sum[:T]
+        xn, y, idx, gate = self.xn[:T], self.y[:T], self.topk_idx[:T], self.topk_gate[:T]
+        xq, xs = (None, None) if few else (self.xq[:T], self.x_scale[:T])
+        L.moe_rmsnorm(dims, x, residual, norm_weight, self.norm_eps,
+                      None if residual is None else stream, xn, xq, xs, None)
+        L.moe_route(dims, xn, wr, self.logits[:T], idx, gate, self.margin[:T], 0.0,
+                    self.near_tie_count, 1, None, None, None, self.workspace)
+        if few:
+            L.moe_token_swiglu(dims, xn, idx, gate, self.w1, self.w1_scale, self.w3,
+                               self.w3_scale, self.w2, self.w2_scale, y, self.workspace)
+            return y, stream
+        L.moe_permute(dims, idx, self.counts, self.offsets, self.pos[:T], self.src_token[:R], None,
+                      None, self.workspace)
+        hq, hs, y_perm = self.hq[:R], self.h_scale[:R], self.y_perm[:R]
+        L.moe_expert_up_mx(dims, xq, xs, self.src_token[:R], self.offsets, self.w1, self.w1_scale,
+                           self.w3, self.w3_scale, hq, hs)
+        L.moe_expert_down_mx(dims, hq, hs, self.offsets, self.w2, self.w2_scale, y_perm)
+        L.moe_combine(dims, y_perm, self.pos[:T], gate, y)
+        return y, stream
