@@ -116,6 +116,25 @@ def test_large_tiles(act, d, f):
     c.check()
 
 
+@pytest.mark.parametrize("T,d,E,f,k,gather", [
+    (100000, 64, 3, 64, 2, True),      # K of half a step: every step is a new tile
+    (60000, 128, 4, 128, 2, False),    # one step to a tile
+    (50000, 192, 5, 64, 3, True),      # two
+    (50000, 384, 2, 64, 2, True),      # three: as many as the ring holds
+    (2000, 64, 16, 1024, 2, True),     # the small tiles
+    (2000, 320, 16, 1024, 2, False),
+])
+def test_workgroups_with_several_tiles(T, d, E, f, k, gather):
+    """more tiles than workgroups on the GPU: the stream of steps runs across them"""
+    print(f"\n[case] experts_mx streams {T} {d} {E} {f} {k} {gather}", flush=True)
+    R = T * k
+    counts = np.random.default_rng(T).multinomial(R - 5, np.ones(E) / E)
+    c = Case(T, d, E, f, k, counts, torch.bfloat16, seed=d, gather=gather)
+    c.upload()
+    c.run()
+    c.check()
+
+
 def test_rows_without_a_table():
     print("\n[case] experts_mx no table", flush=True)
     c = Case(50, 192, 3, 128, 2, [40, 0, 60], torch.bfloat16, seed=1, gather=False)

@@ -5,29 +5,41 @@
 //   UP    a = x W1^T, b = x W3^T, h = silu(a) b, h to 8 bits in the epilogue
 //   DOWN  y_perm = h W2^T
 //
-// v_mfma_scale_f32_32x32x64_f8f6f4 takes both formats and both scales, so
+// v_mfma_scale_f32_16x16x128_f8f6f4 takes both formats and both scales, so
 // nothing is expanded on the way: the tiles stay in 8 and 4 bits in LDS.  With
-// one 8-bit operand it runs at the 8-bit rate, twice that of bf16.
+// one 8-bit operand it runs at the 8-bit rate, twice that of bf16.  On random
+// operands from registers the 16x16x128 form reaches 4.2 PFLOP/s and 32x32x64 3.5
+// (power: both reach 4.7-5.0 on zeros), so the smaller one is used.
 //
-//  * The weights are the first MFMA operand, so a lane holds 16 columns of one
-//    row: the 32 columns of an h block lie in two lanes, and quantising h costs
-//    one exchange between the halves of the wavefront.  fp32 a, b and h are
-//    rounded once, to e4m3.
-//  * An 8-bit operand's lane holds k = 16 g + [0, 16) and 32 + 16 g + [0, 16) of a
-//    64-wide step (g = lane / 32), a 4-bit one k = 32 g + [0, 32); the scale of
-//    block g comes from lane group g in both.
+//  * The weights are the first MFMA operand, so a lane holds columns of one row;
+//    which weight rows its fragments take is chosen so that they lie side by
+//    side (frag_col): an h block is four lanes, and outputs go from registers to
+//    HBM in 8- and 16-byte pieces.  fp32 a, b and h are rounded once, to e4m3.
+//  * An 8-bit operand's lane holds k = 16 q + [0, 16) and 64 + 16 q + [0, 16) of a
+//    128-wide step (q = lane / 16), a 4-bit one k = 32 q + [0, 32); the scale of
+//    block q comes from lane group q in both.
 //  * K steps of 128: a row is 128 bytes of A, 64 of B and one word of scales.
 //    A ring of stages is filled by buffer loads straight into LDS; the 16-byte
-//    chunks are XOR-swizzled through the loads' global addresses (A by
-//    (row >> 1) & 7, B by (row >> 2) & 3), so that 16 rows read at one chunk
-//    hit distinct banks.
+//    chunks are XOR-swizzled through the loads' global addresses, so that the 16
+//    rows of a fragment read at one chunk hit distinct banks.
 //  * Rows past the expert's end, columns past the matrix and the half step at
 //    the end of a K that is no multiple of 128 read zeros through the buffer
 //    bounds; their scales are clamped into range (a scale of row m or column n
 //    reaches only outputs of that row or column).
 //  * One workgroup computes an output in a fixed k order: the results are
 //    bitwise reproducible.
+//
+// Measured at 98304 rows, d = 2048, 64 experts of 1024 (UP and DOWN together,
+// 1.24 TFLOP): one tile per workgroup 709 us; the persistent stream of tiles 650;
+// fills spread between the MFMAs instead of all behind the barrier 612.  Without
+// the epilogues (the exponential and reciprocal of silu, at a quarter of the
+// vector rate, while the matrix cores idle) the same loop takes about 100 us
+// less, without the fills 85 less (the scales' words, one line a row, are half
+// of the lines fetched), and without both and the barriers 390: the rate of the
+// MFMAs at the power limit.  Two workgroups to a CU with 128 x 256 tiles hide the
+// epilogues but fill a third more: 664.
 #include <algorithm>
+#include <type_traits>
 
 #include "mx.h"
 #include "tiles.h"
@@ -37,8 +49,7 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 enum Mode { UP = 0, DOWN = 1 };
 
@@ -63,11 +74,35 @@ struct MxArgs {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* base, int nbytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, nbytes, 0x00020000);
 }
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t voff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)lds, 16, static_cast<int>(voff), 0, 0, 0);
+// Fills of LDS by buffer loads, 16 or 4 bytes a lane, one lane after another from
+// `lds`.  In assembly, since the compiler would hold every later LDS read back
+// for all of them; the waits are ours (wait_vm).  They return nothing to
+// registers.
+__device__ __forceinline__ void dma16(i32x4 r, uint32_t lds, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(voff), "s"(r) : "m0");
 }
-__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t voff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)lds, 4, static_cast<int>(voff), 0, 0, 0);
+__device__ __forceinline__ void dma4(i32x4 r, uint32_t lds, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(voff), "s"(r) : "m0");
+}
+// resource words of [p, p + nbytes), p and nbytes the same in every lane
+__device__ __forceinline__ i32x4 words(const uint8_t* p, int nbytes) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  return i32x4{__builtin_amdgcn_readfirstlane(static_cast<int>(v)),
+               __builtin_amdgcn_readfirstlane(static_cast<int>((v >> 32) & 0xFFFF)),
+               __builtin_amdgcn_readfirstlane(nbytes), 0x00020000};
+}
+__device__ __forceinline__ uint32_t lds_at(const void* p) {
+  return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p)));
+}
+// a pointer that is the same in every lane, in scalar registers
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(hi) << 32 | lo);
 }
 // s_waitcnt with vmcnt = N (N < 64: bits 3-0 and 15-14), expcnt and lgkmcnt left free
 template <int N>
@@ -76,262 +111,416 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
 }
 
-// Tile configurations: WM x WN wavefronts of FM x 2 fragments of 32 x 32.
-template <int FM_, int WM_, int WN_, int NST_>
+// Tile configurations: WM x WN wavefronts of FM x 4 fragments of 16 x 16, a ring
+// of NST stages, PER_CU workgroups resident on a CU.
+template <int FM_, int WM_, int WN_, int NST_, int PER_CU_>
 struct Tile {
-  static constexpr int FM = FM_, WM = WM_, WN = WN_, NST = NST_;
-  static constexpr int BM = 32 * FM * WM, BN = 64 * WN;
+  static constexpr int FM = FM_, WM = WM_, WN = WN_, NST = NST_, PER_CU = PER_CU_;
+  static constexpr int BM = 16 * FM * WM, BN = 64 * WN;
   static constexpr int NW = WM * WN, NT = 64 * NW;
   static constexpr int kA = BM * kStep, kB = BN * kStep / 2, kS = (BM + BN) * 4;
   static constexpr int kStage = kA + kB + kS;
   static constexpr int PA = BM / 8 / NW;                        // fills per wavefront and stage:
   static constexpr int PB = BN / 16 / NW;                       // 1 KB of A, of B,
   static constexpr int PS = ((BM + BN) / 64 + NW - 1) / NW;     // and 64 words of scales
+  static constexpr int kPer = PA + PB + PS;
   static_assert(BM % (8 * NW) == 0 && BN % (16 * NW) == 0 && (BM + BN) % 64 == 0, "whole fills");
+  static_assert(FM % 4 == 0, "a ring of four row fragments");
+  static_assert(NST >= 3, "a stage on its way while the next one is waited for");
 };
-typedef Tile<4, 2, 4, 3> Big;     // 256 x 256
-typedef Tile<2, 1, 4, 3> Small;   // 64 x 256
+typedef Tile<8, 2, 4, 3, 1> Big;     // 256 x 256
+typedef Tile<4, 1, 4, 3, 2> Small;   // 64 x 256
 
-// the four runs of 4 columns that a lane holds of a 32-column fragment (columns
-// 8 q + 4 g + [0, 4)) to 16 consecutive ones (16 g + [0, 16)): one swap between
-// the wavefront's halves per word of each run
-__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
-  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-  a = r[0];
-  b = r[1];
+// stores of a wavefront for one tile (store_tile)
+template <int MODE, typename C, typename OUT>
+constexpr int tile_stores() {
+  return MODE == UP ? 2 * C::FM : C::FM * static_cast<int>(sizeof(OUT));
 }
 
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t r, uint32_t voff, u32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, static_cast<int>(voff), 0, 0);
+}
+
+// largest of a value over the four lanes that share lane % 16
+__device__ __forceinline__ uint32_t max_over_groups(uint32_t v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(b[0], b[1]);
+}
+
+// Which weight row of a wavefront's columns lane r of column fragment j holds:
+// chosen so that a lane's outputs over its fragments lie side by side (UP: 8
+// columns of a and the same of b; DOWN: 16).
+template <int MODE>
+__device__ __forceinline__ int frag_col(int r, int j) {
+  return MODE == UP ? 8 * (r >> 2) + 4 * j + (r & 3) : 16 * (r >> 2) + 4 * j + (r & 3);
+}
+// chunk swizzle of weight row n: distinct for the four runs of a fragment
+template <int MODE>
+__device__ __forceinline__ int w_key(int n) {
+  return (n >> (MODE == UP ? 3 : 4)) & 3;
+}
+
+// The tile's outputs, from registers: lane (r, q) holds row r of each row
+// fragment, and of the wavefront's columns 8 q + [0, 8) (UP) or 16 q + [0, 16).
+// Rows and columns out of range are dropped by the buffer bounds, so every
+// wavefront issues the same number of stores, which the fill counts allow for.
 template <int MODE, typename C, typename OUT>
-__global__ __launch_bounds__(C::NT, 1) void mx_rows_kernel(MxArgs g) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[C::kStage * C::NST];
+__device__ __forceinline__ void store_tile(const MxArgs& g, const f32x4 (&acc)[C::FM][4], int m0,
+                                           int rows, int n0) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));   // nothing of this is kept through the K loop
+  const int r = lane & 15, q = lane >> 4;
+  const int N = g.N;
+  const auto out = rsrc(static_cast<uint8_t*>(g.out) + static_cast<int64_t>(m0) * N * sizeof(OUT),
+                        static_cast<int>(rows * N * sizeof(OUT)));
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i) {
+    __builtin_amdgcn_sched_barrier(0);   // one row fragment's temporaries at a time
+    const int row = wm * 16 * C::FM + i * 16 + r;
+    if constexpr (MODE == UP) {
+      float h[8];
+      uint32_t amax = 0;
+#pragma unroll
+      for (int v = 0; v < 8; ++v) {
+        h[v] = silu_f(acc[i][v / 4][v % 4]) * acc[i][2 + v / 4][v % 4];
+        amax = max(amax, abs_bits(h[v]));
+      }
+      const uint32_t s = mx_scale_byte<kE4M3>(max_over_groups(amax));
+      const float inv = mx_inverse(s);
+      const u32x2 packed = {pack_e4m3(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv),
+                            pack_e4m3(h[4] * inv, h[5] * inv, h[6] * inv, h[7] * inv)};
+      const int n = n0 + wn * 32, ldn = mx_scale_ld(N);
+      __builtin_amdgcn_raw_buffer_store_b64(
+          packed, out,
+          static_cast<int>(row < rows && n < N ? static_cast<uint32_t>(row) * N + n + q * 8
+                                               : kOutOfRange), 0, 0);
+      // a tile's columns are whole words of scales; columns past N pad the last
+      const auto sc = rsrc(g.out_scale + static_cast<int64_t>(m0) * ldn, rows * ldn);
+      __builtin_amdgcn_raw_buffer_store_b8(
+          static_cast<uint8_t>(n < N ? s : 0), sc,
+          static_cast<int>(row < rows && q == 0 && n / 32 < ldn
+                               ? static_cast<uint32_t>(row) * ldn + n / 32 : kOutOfRange), 0, 0);
+    } else {
+      const int n = n0 + wn * 64;
+      const uint32_t at = (static_cast<uint32_t>(row) * N + n + q * 16) * sizeof(OUT);
+      const bool in = row < rows && n < N;
+      if constexpr (sizeof(OUT) == 2) {
+#pragma unroll
+        for (int j = 0; j < 4; j += 2)
+          store16(out, in ? at + j * 8 : kOutOfRange,
+                  u32x4{bf16x2_rne(acc[i][j][0], acc[i][j][1]),
+                        bf16x2_rne(acc[i][j][2], acc[i][j][3]),
+                        bf16x2_rne(acc[i][j + 1][0], acc[i][j + 1][1]),
+                        bf16x2_rne(acc[i][j + 1][2], acc[i][j + 1][3])});
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          store16(out, in ? at + j * 16 : kOutOfRange, __builtin_bit_cast(u32x4, acc[i][j]));
+      }
+    }
+  }
+}
+
+// f(integral_constant 0), ..., f(integral_constant N - 1)
+template <int N, typename F>
+__device__ __forceinline__ void for_each_place(F&& f) {
+  if constexpr (N > 1) for_each_place<N - 1>(f);
+  if constexpr (N > 0) f(std::integral_constant<int, N - 1>{});
+}
+
+// Persistent: a workgroup runs its list of tiles (build_row_sched) as one stream
+// of K steps, so the fills of a tile's first steps are on their way while the
+// last one is multiplied and stored.
+template <int MODE, typename C, typename OUT>
+__global__ __launch_bounds__(C::NT, C::PER_CU * C::NW / 4) void mx_rows_kernel(MxArgs g) {
   constexpr int FM = C::FM, NST = C::NST, BM = C::BM, BN = C::BN, NW = C::NW;
-  const int flat = flat_tile();
-  const int row_tile = flat / g.n_tiles_n, nt = flat - row_tile * g.n_tiles_n;
-  int e, m0, mend;
-  if (!find_row_tile_at<BM>(reinterpret_cast<int*>(lds), g.offsets, g.E, row_tile, &e, &m0, &mend))
-    return;
-  e = __builtin_amdgcn_readfirstlane(e);
-  m0 = __builtin_amdgcn_readfirstlane(m0);
-  mend = __builtin_amdgcn_readfirstlane(mend);
-  __syncthreads();   // every lane holds them before the first fill lands there
-  const int rows = min(BM, mend - m0);
+  constexpr int kRing = C::kStage * NST;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kRing];
+  __shared__ __attribute__((aligned(16))) int4 s_desc[kMaxItems];
+  __shared__ __attribute__((aligned(16))) int32_t s_rows[MODE == UP ? 2 : 1][MODE == UP ? BM : 1];
+  static_assert(sizeof(RowSched) <= kRing, "the schedule is built in the ring");
+  RowSched& sched = *reinterpret_cast<RowSched*>(lds);
+  const int n_items = __builtin_amdgcn_readfirstlane(
+      build_row_sched<BM, C::NT>(sched, g.offsets, g.E, g.n_tiles_n));
+  if (n_items == 0) return;
+  if (threadIdx.x < n_items) s_desc[threadIdx.x] = sched.desc[threadIdx.x];
+  __syncthreads();
+
   const int K = g.K, N = g.N, ldk = mx_scale_ld(K);
-  constexpr int kCols = MODE == UP ? BN / 2 : BN;   // output columns of the tile
-  const int n0 = nt * kCols;
+  constexpr int kCols = MODE == UP ? BN / 2 : BN;   // output columns of a tile
   const int nk = (K + kStep - 1) / kStep;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const bool gather = MODE == UP && g.x_rows;
+  struct Item {
+    int e, m0, rows, n0;
+  };
+  auto item_at = [&](int it) {
+    const int4 d = s_desc[it];
+    Item t;
+    t.e = __builtin_amdgcn_readfirstlane(d.x);
+    t.m0 = __builtin_amdgcn_readfirstlane(d.y);
+    t.rows = min(BM, __builtin_amdgcn_readfirstlane(d.z) - t.m0);
+    t.n0 = __builtin_amdgcn_readfirstlane(d.w) * kCols;
+    return t;
+  };
+  auto join = [&] {   // every wavefront's reads and waits so far, before what follows
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
 
-  // ---- fills: global offsets of this wavefront's lanes, and the last step's
-  // where K ends in half a step
+  // ---- fills: this wavefront's global offsets for the tile being filled
   uint32_t va[C::PA], vb[C::PB], vs[C::PS];
-  uint32_t last_a = 0, last_b = 0;   // bit u: out of range in the half step
+  uint32_t last_a = 0, last_b = 0;   // bit u: past K in a half step
 #pragma unroll
   for (int u = 0; u < C::PA; ++u) {
     const int row = (wave * C::PA + u) * 8 + (lane >> 3);
-    const int chunk = (lane & 7) ^ ((row >> 1) & 7);
-    const int src = MODE == UP && g.x_rows ? g.x_rows[min(m0 + row, mend - 1)] : row;
-    va[u] = row < rows ? static_cast<uint32_t>(src) * K + chunk * 16 : kOutOfRange;
-    last_a |= (chunk >= 4 ? 1u : 0u) << u;
+    last_a |= (((lane & 7) ^ ((row >> 1) & 7)) >= 4 ? 1u : 0u) << u;
   }
 #pragma unroll
   for (int u = 0; u < C::PB; ++u) {
     const int row = (wave * C::PB + u) * 16 + (lane >> 2);
-    const int chunk = (lane & 3) ^ ((row >> 2) & 3);
-    const int n = row & (kCols - 1);
-    vb[u] = n0 + n < N ? static_cast<uint32_t>(n) * (K / 2) + chunk * 16 : kOutOfRange;
-    last_b |= (chunk >= 2 ? 1u : 0u) << u;
+    last_b |= (((lane & 3) ^ w_key<MODE>(row)) >= 2 ? 1u : 0u) << u;
   }
-  const int64_t wrow = static_cast<int64_t>(e) * N + n0;   // first weight row of the tile
-  const bool gather = MODE == UP && g.x_rows;
-  const uint8_t* abase = gather ? g.a : g.a + static_cast<int64_t>(m0) * K;
-  const int abytes = static_cast<int>(gather ? g.x_tokens * K : static_cast<int64_t>(rows) * K);
   const bool second = MODE == UP && wave * C::PB * 16 >= kCols;   // this wavefront fills W3
-  const uint8_t* bbase = (second ? g.w1 : g.w0) + wrow * (K / 2);
-  const int bbytes = min(kCols, N - n0) * (K / 2);
-  const uint8_t* sbase[C::PS];
-  int sbytes[C::PS], sslot[C::PS];
+  const uint8_t *abase = g.a, *bbase = g.w0, *sbase[C::PS];
+  int abytes = 0, bbytes = 0, sbytes[C::PS], sslot[C::PS];
 #pragma unroll
-  for (int u = 0; u < C::PS; ++u) {
-    // the fills past the last one repeat it (every wavefront issues as many)
+  for (int u = 0; u < C::PS; ++u)   // the fills past the last one repeat it
     sslot[u] = min(wave + u * NW, (BM + BN) / 64 - 1);
-    const int row = sslot[u] * 64 + lane;
-    if (sslot[u] * 64 < BM) {
-      const int at = min(m0 + row, mend - 1);
-      const int src = gather ? g.x_rows[at] : at - m0;
-      sbase[u] = gather ? g.a_scale : g.a_scale + static_cast<int64_t>(m0) * ldk;
-      sbytes[u] = static_cast<int>(gather ? g.x_tokens * ldk : static_cast<int64_t>(rows) * ldk);
-      vs[u] = static_cast<uint32_t>(src) * ldk;
-    } else {
-      const int b = row - BM, n = min(b & (kCols - 1), N - 1 - n0);
-      sbase[u] = (sslot[u] * 64 - BM >= kCols ? g.w1_scale : g.w0_scale) + wrow * ldk;
-      sbytes[u] = min(kCols, N - n0) * ldk;
-      vs[u] = static_cast<uint32_t>(n) * ldk;
+  int fill_item = 0, fill_kt = 0;
+  const uint32_t lds_base = lds_at(lds);
+  // the gather table of tile `it` into its half of s_rows
+  auto fetch_rows = [&](int it) {
+    if constexpr (MODE == UP) {
+      if (!gather || it >= n_items) return;
+      const Item t = item_at(it);
+      for (int p = wave; p < BM / 64; p += NW)
+        dma4(words(reinterpret_cast<const uint8_t*>(g.x_rows + t.m0), t.rows * 4),
+             lds_at(&s_rows[it & 1][p * 64]), (p * 64 + lane) * 4);
     }
-  }
-  auto issue = [&](int kt, int slot) {
-    uint8_t* st = lds + slot * C::kStage;
+  };
+  auto aim = [&](int it) {   // the offsets of tile `it`; its gather table has landed
+    const Item t = item_at(it);
+    int lane = tid & 63;
+    asm volatile("" : "+v"(lane));   // computed here, not kept through the K loop
+    auto source = [&](int row) {
+      return static_cast<uint32_t>(MODE == UP ? s_rows[it & 1][row] : row);
+    };
+#pragma unroll
+    for (int u = 0; u < C::PA; ++u) {
+      const int row = (wave * C::PA + u) * 8 + (lane >> 3);
+      const int chunk = (lane & 7) ^ ((row >> 1) & 7);
+      const uint32_t from = source(row) * K + chunk * 16;
+      va[u] = row < t.rows ? from : kOutOfRange;
+    }
+#pragma unroll
+    for (int u = 0; u < C::PB; ++u) {
+      const int row = (wave * C::PB + u) * 16 + (lane >> 2);
+      const int chunk = (lane & 3) ^ w_key<MODE>(row);
+      const int n = row & (kCols - 1);
+      vb[u] = t.n0 + n < N ? static_cast<uint32_t>(n) * (K / 2) + chunk * 16 : kOutOfRange;
+    }
+    const int64_t wrow = static_cast<int64_t>(t.e) * N + t.n0;   // first weight row of the tile
+    abase = uniform(gather ? g.a : g.a + static_cast<int64_t>(t.m0) * K);
+    abytes = static_cast<int>(gather ? g.x_tokens * K : static_cast<int64_t>(t.rows) * K);
+    bbase = uniform((second ? g.w1 : g.w0) + wrow * (K / 2));
+    bbytes = min(kCols, N - t.n0) * (K / 2);
+#pragma unroll
+    for (int u = 0; u < C::PS; ++u) {
+      const int row = sslot[u] * 64 + lane;
+      if (sslot[u] * 64 < BM) {
+        sbase[u] = uniform(gather ? g.a_scale : g.a_scale + static_cast<int64_t>(t.m0) * ldk);
+        sbytes[u] = static_cast<int>(gather ? g.x_tokens * ldk : static_cast<int64_t>(t.rows) * ldk);
+        vs[u] = source(min(row, t.rows - 1)) * ldk;
+      } else {
+        const int b = row - BM;
+        sbase[u] = uniform((sslot[u] * 64 - BM >= kCols ? g.w1_scale : g.w0_scale) + wrow * ldk);
+        sbytes[u] = min(kCols, N - t.n0) * ldk;
+        vs[u] = static_cast<uint32_t>(min(b & (kCols - 1), N - 1 - t.n0)) * ldk;
+      }
+    }
+  };
+  // the u-th fill of the stream's next step, into ring slot `slot`
+  auto fill = [&](auto which, int slot) {
+    constexpr int u = decltype(which)::value;
+    const uint32_t st = lds_base + slot * C::kStage;
+    const int kt = fill_kt;
     const bool half = (kt + 1) * kStep > K;
-    const auto ra = rsrc(abase + kt * kStep, abytes - kt * kStep);
-#pragma unroll
-    for (int u = 0; u < C::PA; ++u)
-      dma16(ra, st + (wave * C::PA + u) * 1024,
+    if constexpr (u < C::PA) {
+      dma16(words(abase + kt * kStep, abytes - kt * kStep), st + (wave * C::PA + u) * 1024,
             half && ((last_a >> u) & 1) ? kOutOfRange : va[u]);
-    const auto rb = rsrc(bbase + kt * (kStep / 2), bbytes - kt * (kStep / 2));
+    } else if constexpr (u < C::PA + C::PB) {
+      constexpr int n = u - C::PA;
+      dma16(words(bbase + kt * (kStep / 2), bbytes - kt * (kStep / 2)),
+            st + C::kA + (wave * C::PB + n) * 1024,
+            half && ((last_b >> n) & 1) ? kOutOfRange : vb[n]);
+    } else if constexpr (u < C::kPer) {
+      constexpr int n = u - C::PA - C::PB;
+      dma4(words(sbase[n] + kt * 4, sbytes[n] - kt * 4), st + C::kA + C::kB + sslot[n] * 256,
+           vs[n]);
+    }
+  };
+  // To the stream's next step.  A new tile's gather table was fetched a tile ago:
+  // with NST steps to a tile it has landed.  Past the last tile the fills go on,
+  // out of range (zeros, no memory read), so that the counts below stay right.
+  auto advance = [&] {
+    if (++fill_kt < nk) return;
+    fill_kt = 0;
+    if (++fill_item < n_items) {
+      if (gather && nk < NST) {
+        wait_vm<0>();
+        join();
+      }
+      aim(fill_item);
+      fetch_rows(fill_item + 1);
+    } else {
 #pragma unroll
-    for (int u = 0; u < C::PB; ++u)
-      dma16(rb, st + C::kA + (wave * C::PB + u) * 1024,
-            half && ((last_b >> u) & 1) ? kOutOfRange : vb[u]);
+      for (int u = 0; u < C::PA; ++u) va[u] = kOutOfRange;
 #pragma unroll
-    for (int u = 0; u < C::PS; ++u)
-      dma4(rsrc(sbase[u] + kt * 4, sbytes[u] - kt * 4), st + C::kA + C::kB + sslot[u] * 256, vs[u]);
+      for (int u = 0; u < C::PB; ++u) vb[u] = kOutOfRange;
+#pragma unroll
+      for (int u = 0; u < C::PS; ++u) vs[u] = kOutOfRange;
+    }
   };
 
   // ---- fragments
   const int wm = wave / C::WN, wn = wave % C::WN;
-  const int r = lane & 31, gq = lane >> 5;
-  f32x16 acc[FM][2];
+  const int r = lane & 15, q = lane >> 4;
+  f32x4 acc[FM][4];
+  constexpr int kFragW = MODE == UP ? 2 : 4;   // column fragments of one matrix
+  const int wcol = wn * 16 * kFragW + frag_col<MODE>(r, 0);
+  const uint32_t aoff0 = (wm * 16 * FM + r) * kStep + ((q ^ ((r >> 1) & 7)) * 16);
+  const uint32_t aoff1 = (wm * 16 * FM + r) * kStep + (((4 + q) ^ ((r >> 1) & 7)) * 16);
+  const uint32_t boff = C::kA + wcol * (kStep / 2) + ((q ^ w_key<MODE>(wcol)) * 16);
+  const uint32_t sxoff = C::kA + C::kB + (wm * 16 * FM + r) * 4;
+  const uint32_t swoff = C::kA + C::kB + (BM + wcol) * 4;
+  // Row fragments go through a ring of four, read two ahead of their MFMAs; the
+  // column fragments of the next step are read beside the last row fragments.
+  i32x8 x[4];
+  int sx[4];
+  i32x4 w[4], w_next[4];
+  int sw[4], sw_next[4];
+  auto read_x = [&](uint32_t st, int i, int to) {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(lds + st + aoff0 + i * 16 * kStep);
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(lds + st + aoff1 + i * 16 * kStep);
+    x[to] = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    sx[to] = *reinterpret_cast<const int*>(lds + st + sxoff + i * 64);
+  };
+  auto read_w = [&](uint32_t st) {
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+    for (int j = 0; j < 4; ++j) {
+      const int row = j < kFragW ? 4 * j : kCols + 4 * (j - kFragW);
+      w_next[j] = *reinterpret_cast<const i32x4*>(lds + st + boff + row * (kStep / 2));
+      sw_next[j] = *reinterpret_cast<const int*>(lds + st + swoff + row * 4);
+    }
+  };
+  auto take_w = [&] {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
-  uint32_t aoff[4], boff[2];   // byte offsets of the lane's chunks in a stage
+    for (int j = 0; j < 4; ++j) {
+      w[j] = w_next[j];
+      sw[j] = sw_next[j] >> (8 * q);   // the lane group's block
+    }
+  };
+  auto multiply = [&](int i, auto first, auto reads) {
+    const int s = sx[i % 4] >> (8 * q);
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-    aoff[c] = (wm * 32 * FM + r) * kStep + (((2 * c + gq) ^ ((r >> 1) & 7)) * 16);
+    for (int j = 0; j < 4; ++j) {
+      const i32x8 wf = {w[j][0], w[j][1], w[j][2], w[j][3], 0, 0, 0, 0};
+      const f32x4 c = decltype(first)::value ? f32x4{} : acc[i][j];
+      acc[i][j] =
+          __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, x[i % 4], c, 4, 0, 0, sw[j], 0, s);
+    }
+    // keeps the MFMAs where they stand among the reads, waits and barriers (they
+    // touch no memory, so the compiler would sink them all behind the branches)
+    asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]), "+v"(acc[i][2]), "+v"(acc[i][3]));
+    // the matrix cores first, `reads` LDS reads behind each MFMA
+    if constexpr (decltype(reads)::value > 0) {
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
-    boff[c] = C::kA + (wn * 32 + r) * (kStep / 2) + (((2 * c + gq) ^ ((r >> 2) & 3)) * 16);
-  const uint32_t soff = C::kA + C::kB;
-
-#pragma unroll
-  for (int s = 0; s < NST - 1; ++s)
-    if (s < nk) issue(s, s);
-  constexpr int kPer = C::PA + C::PB + C::PS;
-  int slot = 0;
-  for (int kt = 0; kt < nk; ++kt) {
-    // stage kt has landed when at most the fills of the later stages are out
-    if (kt + NST - 2 < nk) wait_vm<(NST - 2) * kPer>();
-    else wait_vm<0>();
-    // landed for all, and stage kt - 1 read by all (its reads are waited for
-    // here, wherever the compiler has put the MFMAs that use them)
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    if (kt + NST - 1 < nk) issue(kt + NST - 1, slot == 0 ? NST - 1 : slot - 1);
-    const uint8_t* st = lds + slot * C::kStage;
-    int sx[FM], sw[2];
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-      sx[i] = *reinterpret_cast<const int*>(st + soff + (wm * 32 * FM + i * 32 + r) * 4) >> (8 * gq);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      sw[j] = *reinterpret_cast<const int*>(st + soff + (BM + j * (BN / 2) + wn * 32 + r) * 4) >>
-              (8 * gq);
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      i32x8 wf[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const i32x4 b =
-            *reinterpret_cast<const i32x4*>(st + boff[kk] + j * (BN / 2) * (kStep / 2));
-        wf[j] = i32x8{b[0], b[1], b[2], b[3], 0, 0, 0, 0};
-      }
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const i32x4 lo = *reinterpret_cast<const i32x4*>(st + aoff[2 * kk] + i * 32 * kStep);
-        const i32x4 hi = *reinterpret_cast<const i32x4*>(st + aoff[2 * kk + 1] + i * 32 * kStep);
-        const i32x8 xf = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (kk == 0)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[j], xf, acc[i][j], 4, 0,
-                                                                        0, sw[j], 0, sx[i]);
-          else
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[j], xf, acc[i][j], 4, 0,
-                                                                        2, sw[j], 2, sx[i]);
-        }
+      for (int j = 0; j < 4; ++j) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, decltype(reads)::value, 0);
       }
     }
-    slot = slot + 1 == NST ? 0 : slot + 1;
-  }
+    __builtin_amdgcn_sched_barrier(0);
+  };
 
-  // ---- epilogue, from registers: lane (r, gq) holds columns 8 q + 4 gq + [0, 4)
-  // of row r of each fragment
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int row = wm * 32 * FM + i * 32 + r;
-    const int64_t m = m0 + row;
-    if constexpr (MODE == UP) {
-      float h[16];
-      uint32_t amax = 0;
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        h[v] = silu_f(acc[i][0][v]) * acc[i][1][v];
-        amax = max(amax, abs_bits(h[v]));
-      }
-      uint32_t other = amax;
-      swap_halves(amax, other);
-      const uint32_t s = mx_scale_byte<kE4M3>(max(amax, other));
-      const float inv = mx_inverse(s);
-      uint32_t q[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        q[c] = pack_e4m3(h[4 * c] * inv, h[4 * c + 1] * inv, h[4 * c + 2] * inv,
-                         h[4 * c + 3] * inv);
-      swap_halves(q[0], q[2]);
-      swap_halves(q[1], q[3]);
-      const int n = n0 + wn * 32, ldn = mx_scale_ld(N);
-      if (row < rows) {
-        if (n < N)
-          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(g.out) + m * N + n + gq * 16) =
-              make_uint4(q[0], q[2], q[1], q[3]);
-        // a tile's 128 columns are one word of scales; columns past N pad it
-        if (gq == 0 && n / 32 < ldn)
-          g.out_scale[m * ldn + n / 32] = static_cast<uint8_t>(n < N ? s : 0);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int n = n0 + j * (BN / 2) + wn * 32;
-        OUT* out = static_cast<OUT*>(g.out) + m * N + n + gq * 16;
-        if constexpr (sizeof(OUT) == 2) {
-          uint32_t lo[4], hi[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            lo[c] = bf16x2_rne(acc[i][j][4 * c], acc[i][j][4 * c + 1]);
-            hi[c] = bf16x2_rne(acc[i][j][4 * c + 2], acc[i][j][4 * c + 3]);
-          }
-          swap_halves(lo[0], lo[2]);
-          swap_halves(hi[0], hi[2]);
-          swap_halves(lo[1], lo[3]);
-          swap_halves(hi[1], hi[3]);
-          if (row < rows && n < N) {
-            reinterpret_cast<uint4*>(out)[0] = make_uint4(lo[0], hi[0], lo[2], hi[2]);
-            reinterpret_cast<uint4*>(out)[1] = make_uint4(lo[1], hi[1], lo[3], hi[3]);
-          }
-        } else {
-          uint32_t t[4][4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) t[c][v] = __float_as_uint(acc[i][j][4 * c + v]);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            swap_halves(t[0][v], t[2][v]);
-            swap_halves(t[1][v], t[3][v]);
-          }
-          if (row < rows && n < N) {
-            const int order[4] = {0, 2, 1, 3};
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              reinterpret_cast<uint4*>(out)[c] =
-                  make_uint4(t[order[c]][0], t[order[c]][1], t[order[c]][2], t[order[c]][3]);
-          }
-        }
-      }
-    }
+  // ---- the stream
+  // A step's fills go out a few at a time between its MFMAs (all at once they
+  // queue behind each other while the matrix cores idle): places 0 and 1 behind
+  // the join that frees the slot, the others in the next step, before its join.
+  constexpr int kEach = (C::kPer + FM - 1) / FM;   // fills of a place
+  auto fills = [&](auto place, int slot) {
+    constexpr int p = decltype(place)::value;
+    fill(std::integral_constant<int, p * kEach>{}, slot);
+    if constexpr (kEach > 1) fill(std::integral_constant<int, p * kEach + 1>{}, slot);
+    static_assert(kEach <= 2, "fills of a place");
+  };
+  if constexpr (MODE == UP) {
+    if (!gather)
+      for (int p = tid; p < 2 * BM; p += C::NT) s_rows[p / BM][p % BM] = p % BM;
+    fetch_rows(0);
+    wait_vm<0>();
+    join();
   }
+  aim(0);
+  fetch_rows(1);
+  for (int s = 0; s < NST - 1; ++s) {
+    for_each_place<FM>([&](auto place) { fills(place, s); });
+    advance();
+  }
+  fills(std::integral_constant<int, 0>{}, NST - 1);
+  fills(std::integral_constant<int, 1>{}, NST - 1);
+  wait_vm<0>();
+  join();
+  read_w(0);
+  read_x(0, 0, 0);
+  read_x(0, 1, 1);
+  take_w();
+  int slot = 0, filling = NST - 1;
+  // One step.  Its last two row fragments run behind the join: by then it has
+  // been read by all (their operands are in registers) and the next step has
+  // landed for all; the step NST on is filled in its place.  `stored`: the
+  // stores of the tile before are newer than the fills that are waited for.
+  auto step = [&](auto first, bool stored) {
+    const uint32_t st = slot * C::kStage;
+    const int next = slot + 1 == NST ? 0 : slot + 1;
+    const uint32_t sn = next * C::kStage;
+    for_each_place<FM - 2>([&](auto place) {
+      constexpr int i = decltype(place)::value;
+      read_x(st, i + 2, (i + 2) % 4);
+      fills(std::integral_constant<int, i + 2>{}, filling);
+      multiply(i, first, std::integral_constant<int, 1>{});
+    });
+    advance();
+    if (decltype(first)::value && stored) wait_vm<(NST - 2) * C::kPer + tile_stores<MODE, C, OUT>()>();
+    else wait_vm<(NST - 2) * C::kPer>();
+    join();
+    filling = slot;
+    read_w(sn);
+    read_x(sn, 0, FM % 4);
+    read_x(sn, 1, (FM + 1) % 4);
+    fills(std::integral_constant<int, 0>{}, filling);
+    multiply(FM - 2, first, std::integral_constant<int, 4>{});
+    fills(std::integral_constant<int, 1>{}, filling);
+    multiply(FM - 1, first, std::integral_constant<int, 0>{});
+    take_w();
+    slot = next;
+  };
+  for (int it = 0; it < n_items; ++it) {
+    step(std::integral_constant<bool, true>{}, it > 0);
+    for (int kt = 1; kt < nk; ++kt) step(std::integral_constant<bool, false>{}, false);
+    const Item t = item_at(it);
+    store_tile<MODE, C, OUT>(g, acc, t.m0, t.rows, t.n0);
+  }
+  wait_vm<0>();   // no fill may land after the workgroup's end
 }
 
 // workgroups that cover any split of the rows over the experts: an expert's last
@@ -349,7 +538,9 @@ hipError_t run_rows(MxArgs g, const moe_dims& dm, hipStream_t s) {
   constexpr int kCols = MODE == UP ? C::BN / 2 : C::BN;
   g.n_tiles_n = (g.N + kCols - 1) / kCols;
   const int64_t tiles = grid_tiles<MODE, C>(dm, g.N);
-  hipLaunchKernelGGL((mx_rows_kernel<MODE, C, OUT>), dim3(static_cast<unsigned>(tiles)),
+  const int64_t grid = std::max(std::min(tiles, int64_t(256 * C::PER_CU)),   // what 256 CUs hold
+                                (tiles + kMaxItems * kXcd - 1) / (kMaxItems * kXcd) * kXcd);
+  hipLaunchKernelGGL((mx_rows_kernel<MODE, C, OUT>), dim3(static_cast<unsigned>(grid)),
                      dim3(C::NT), 0, s, g);
   return hipGetLastError();
 }
