@@ -659,45 +659,57 @@ _FORMATS = {"e4m3": (MOE_MX_E4M3, 1), "e2m1": (MOE_MX_E2M1, 2)}   # code, elemen
 
 
 def _arg(t, name, dtypes, numel, device):
-    """Pointer of a contiguous tensor of `numel` values on `device`; None stays NULL."""
+    """Pointer of a contiguous tensor of `numel` values on GPU `device` (an index);
+    None stays NULL."""
     if t is None:
         return None
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, is on {t.device}")
+    if (t.dtype in dtypes and t.numel() == numel and t.get_device() == device
+            and t.is_contiguous()):
+        return t.data_ptr()
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, is on {t.device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.numel() != numel:
         raise ValueError(f"{name} must hold {numel} values, has shape {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _device_of(t, name):
     if t is None or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    return t.device
+    return t.get_device()
 
 
 def _workspace(t, device):
     """(pointer, bytes) of a workspace tensor; None is no workspace."""
     if t is None:
         return None, 0
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {device}")
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on cuda:{device}")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _enqueue(func, device, stream, *args):
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
+    """Runs an entry point on GPU `device`: on its current stream unless one is given."""
+    raw = (torch._C._cuda_getCurrentRawStream(device) if stream is None   # 2 us less than
+           else stream.cuda_stream)                                       # current_stream()
     fn = getattr(lib(), func)
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, stream.cuda_stream)
+    if device == torch.cuda.current_device():
+        st = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            st = fn(*args, stream.cuda_stream)
-    _check(st, func)
+            st = fn(*args, raw)
+    if st != 0:
+        _check(st, func)
+
+
+def _scale_cols(cols):
+    return (cols + 127) // 128 * 4
+
+
+_ACT = {MOE_F32: (torch.float32,), MOE_BF16: (torch.bfloat16,)}
+_F32T, _I32T, _U8 = (torch.float32,), (torch.int32,), (torch.uint8,)
 
 
 def moe_mx_scale_cols(cols) -> int:
@@ -742,15 +754,14 @@ def moe_mx_dequantize(q, scale, fmt, dst, stream=None):
 
 def moe_rmsnorm(dims, x, residual, weight, eps, sum_out, y, q, q_scale, rstd, stream=None):
     device = _device_of(x, "x")
-    act, T, d = (act_dtype(dims),), dims.T, dims.d
-    f32 = (torch.float32,)
+    act, T, d = _ACT.get(dims.act, ()), dims.T, dims.d
     _enqueue("moe_rmsnorm", device, stream, ctypes.byref(dims),
              _arg(x, "x", act, T * d, device), _arg(residual, "residual", act, T * d, device),
-             _arg(weight, "weight", f32, d, device), float(eps),
+             _arg(weight, "weight", _F32T, d, device), float(eps),
              _arg(sum_out, "sum", act, T * d, device), _arg(y, "y", act, T * d, device),
              _arg(q, "q", _BYTES, T * d, device),
-             _arg(q_scale, "q_scale", _BYTES, T * moe_mx_scale_cols(d), device),
-             _arg(rstd, "rstd", f32, T, device))
+             _arg(q_scale, "q_scale", _BYTES, T * _scale_cols(d), device),
+             _arg(rstd, "rstd", _F32T, T, device))
 
 
 def moe_rmsnorm_bwd_workspace_bytes(dims) -> int:
@@ -759,34 +770,33 @@ def moe_rmsnorm_bwd_workspace_bytes(dims) -> int:
 
 def moe_rmsnorm_bwd(dims, dy, s, weight, rstd, dsum, dx, dweight, workspace, stream=None):
     device = _device_of(dy, "dy")
-    act, T, d = (act_dtype(dims),), dims.T, dims.d
-    f32 = (torch.float32,)
+    act, T, d = _ACT.get(dims.act, ()), dims.T, dims.d
     _enqueue("moe_rmsnorm_bwd", device, stream, ctypes.byref(dims),
              _arg(dy, "dy", act, T * d, device), _arg(s, "s", act, T * d, device),
-             _arg(weight, "weight", f32, d, device), _arg(rstd, "rstd", f32, T, device),
+             _arg(weight, "weight", _F32T, d, device), _arg(rstd, "rstd", _F32T, T, device),
              _arg(dsum, "dsum", act, T * d, device), _arg(dx, "dx", act, T * d, device),
-             _arg(dweight, "dweight", f32, d, device), *_workspace(workspace, device))
+             _arg(dweight, "dweight", _F32T, d, device), *_workspace(workspace, device))
 
 
 def _mx_weight(w, w_scale, name, E, n, width, device):
-    return (_arg(w, name, (torch.uint8,), E * n * width // 2, device),
-            _arg(w_scale, name + "_scale", _BYTES, E * n * moe_mx_scale_cols(width), device))
+    return (_arg(w, name, _U8, E * n * width // 2, device),
+            _arg(w_scale, name + "_scale", _BYTES, E * n * _scale_cols(width), device))
 
 
 def moe_expert_up_mx(dims, xq, x_scale, src_token, expert_offsets, w1, w1_scale, w3, w3_scale,
                      hq, h_scale, stream=None):
     device = _device_of(xq, "xq")
     T, d, E, f, R = dims.T, dims.d, dims.E, dims.f, dims.T * dims.k
-    i32, rows = (torch.int32,), R if src_token is None else T
+    rows = R if src_token is None else T
     _enqueue("moe_expert_up_mx", device, stream, ctypes.byref(dims),
              _arg(xq, "xq", _BYTES, rows * d, device),
-             _arg(x_scale, "x_scale", _BYTES, rows * moe_mx_scale_cols(d), device),
-             _arg(src_token, "src_token", i32, R, device),
-             _arg(expert_offsets, "expert_offsets", i32, E + 1, device),
+             _arg(x_scale, "x_scale", _BYTES, rows * _scale_cols(d), device),
+             _arg(src_token, "src_token", _I32T, R, device),
+             _arg(expert_offsets, "expert_offsets", _I32T, E + 1, device),
              *_mx_weight(w1, w1_scale, "w1", E, f, d, device),
              *_mx_weight(w3, w3_scale, "w3", E, f, d, device),
              _arg(hq, "hq", _BYTES, R * f, device),
-             _arg(h_scale, "h_scale", _BYTES, R * moe_mx_scale_cols(f), device))
+             _arg(h_scale, "h_scale", _BYTES, R * _scale_cols(f), device))
 
 
 def moe_expert_down_mx(dims, hq, h_scale, expert_offsets, w2, w2_scale, y_perm, stream=None):
@@ -794,10 +804,10 @@ def moe_expert_down_mx(dims, hq, h_scale, expert_offsets, w2, w2_scale, y_perm, 
     d, E, f, R = dims.d, dims.E, dims.f, dims.T * dims.k
     _enqueue("moe_expert_down_mx", device, stream, ctypes.byref(dims),
              _arg(hq, "hq", _BYTES, R * f, device),
-             _arg(h_scale, "h_scale", _BYTES, R * moe_mx_scale_cols(f), device),
-             _arg(expert_offsets, "expert_offsets", (torch.int32,), E + 1, device),
+             _arg(h_scale, "h_scale", _BYTES, R * _scale_cols(f), device),
+             _arg(expert_offsets, "expert_offsets", _I32T, E + 1, device),
              *_mx_weight(w2, w2_scale, "w2", E, d, f, device),
-             _arg(y_perm, "y_perm", (act_dtype(dims),), R * d, device))
+             _arg(y_perm, "y_perm", _ACT.get(dims.act, ()), R * d, device))
 
 
 def moe_token_swiglu_workspace_bytes(dims) -> int:
@@ -807,10 +817,10 @@ def moe_token_swiglu_workspace_bytes(dims) -> int:
 def moe_token_swiglu(dims, x, topk_idx, topk_gate, w1, w1_scale, w3, w3_scale, w2, w2_scale, y,
                      workspace, stream=None):
     device = _device_of(x, "x")
-    act, T, d, E, f, R = (act_dtype(dims),), dims.T, dims.d, dims.E, dims.f, dims.T * dims.k
+    act, T, d, E, f, R = _ACT.get(dims.act, ()), dims.T, dims.d, dims.E, dims.f, dims.T * dims.k
     _enqueue("moe_token_swiglu", device, stream, ctypes.byref(dims),
-             _arg(x, "x", act, T * d, device), _arg(topk_idx, "topk_idx", (torch.int32,), R, device),
-             _arg(topk_gate, "topk_gate", (torch.float32,), R, device),
+             _arg(x, "x", act, T * d, device), _arg(topk_idx, "topk_idx", _I32T, R, device),
+             _arg(topk_gate, "topk_gate", _F32T, R, device),
              *_mx_weight(w1, w1_scale, "w1", E, f, d, device),
              *_mx_weight(w3, w3_scale, "w3", E, f, d, device),
              *_mx_weight(w2, w2_scale, "w2", E, d, f, device),
