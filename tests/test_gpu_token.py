@@ -67,6 +67,9 @@ SHAPES = [   # T, d, E, f, k
     (1, 64, 1, 64, 1), (1, 2048, 64, 1024, 6), (1, 192, 8, 320, 2), (2, 128, 4, 64, 4),
     (7, 256, 8, 256, 2), (16, 576, 16, 192, 4), (33, 128, 2, 192, 2), (100, 64, 3, 128, 1),
     (64, 192, 256, 64, 16), (37, 320, 23, 64, 5), (5, 1088, 64, 128, 7),
+    # either side of the two ways, K of several batches, experts of over 16 tokens
+    (8, 1600, 4, 1088, 2), (9, 1600, 4, 1088, 2), (8, 64, 16, 64, 16), (60, 1024, 3, 576, 2),
+    (9, 2560, 40, 64, 3),
 ]
 
 

@@ -278,7 +278,7 @@ class MoEServeLayer:
     """
 
     def __init__(self, max_tokens: int, d: int, E: int, f: int, k: int, act: torch.dtype,
-                 norm_eps: float = 1e-6, few_slots: int = 256, device="cuda"):
+                 norm_eps: float = 1e-6, few_slots: int = 128, device="cuda"):
         self.T, self.d, self.E, self.f, self.k, self.act = max_tokens, d, E, f, k, act
         self.norm_eps = float(norm_eps)
         self.few_slots = min(int(few_slots), L.MOE_TOKEN_MAX_SLOTS)
