@@ -135,6 +135,20 @@ def test_workgroups_with_several_tiles(T, d, E, f, k, gather):
     c.check()
 
 
+@pytest.mark.parametrize("T,d,E,f,gather", [(8000, 576, 60, 512, True), (10000, 512, 3, 1088, False)])
+def test_large_tiles_of_few_rows(T, d, E, f, gather):
+    """large tiles whose second half of wavefronts has no rows, before and after
+    full ones, several to a workgroup"""
+    print(f"\n[case] experts_mx few rows {T} {d} {E} {f} {gather}", flush=True)
+    counts = np.random.default_rng(d).integers(0, 300, size=E)
+    counts[::4] = [128, 0, 129, 1, 256][:len(counts[::4])] * 3 if E == 60 else 100
+    counts[E // 2] = 2 * T - 3 - (counts.sum() - counts[E // 2])
+    c = Case(T, d, E, f, 2, counts, torch.bfloat16, seed=d, gather=gather)
+    c.upload()
+    c.run()
+    c.check()
+
+
 def test_rows_without_a_table():
     print("\n[case] experts_mx no table", flush=True)
     c = Case(50, 192, 3, 128, 2, [40, 0, 60], torch.bfloat16, seed=1, gather=False)

@@ -31,7 +31,8 @@
 //
 // Measured at 98304 rows, d = 2048, 64 experts of 1024 (UP and DOWN together,
 // 1.24 TFLOP): one tile per workgroup 709 us; the persistent stream of tiles 650;
-// fills spread between the MFMAs instead of all behind the barrier 612.  Without
+// fills spread between the MFMAs instead of all behind the barrier 612, and without
+// the MFMAs of wavefronts past a tile's rows 608.  Without
 // the epilogues (the exponential and reciprocal of silu, at a quarter of the
 // vector rate, while the matrix cores idle) the same loop takes about 100 us
 // less, without the fills 85 less (the scales' words, one line a row, are half
@@ -296,7 +297,7 @@ __global__ __launch_bounds__(C::NT, C::PER_CU * C::NW / 4) void mx_rows_kernel(M
   for (int u = 0; u < C::PS; ++u)   // the fills past the last one repeat it
     sslot[u] = min(wave + u * NW, (BM + BN) / 64 - 1);
   int fill_item = 0, fill_kt = 0;
-  const uint32_t lds_base = lds_at(lds);
+  const uint32_t lds_base = lds_at(lds), rows_base = lds_at(s_rows);
   // the gather table of tile `it` into its half of s_rows
   auto fetch_rows = [&](int it) {
     if constexpr (MODE == UP) {
@@ -304,7 +305,7 @@ __global__ __launch_bounds__(C::NT, C::PER_CU * C::NW / 4) void mx_rows_kernel(M
       const Item t = item_at(it);
       for (int p = wave; p < BM / 64; p += NW)
         dma4(words(reinterpret_cast<const uint8_t*>(g.x_rows + t.m0), t.rows * 4),
-             lds_at(&s_rows[it & 1][p * 64]), (p * 64 + lane) * 4);
+             rows_base + ((it & 1) * BM + p * 64) * 4, (p * 64 + lane) * 4);
     }
   };
   auto aim = [&](int it) {   // the offsets of tile `it`; its gather table has landed
@@ -514,10 +515,35 @@ __global__ __launch_bounds__(C::NT, C::PER_CU * C::NW / 4) void mx_rows_kernel(M
     take_w();
     slot = next;
   };
+  // A step of a tile without rows for this wavefront: its share of the fills (a
+  // tile of 128 rows of 256 then costs 4% to 15% less; skipping single row fragments
+  // breaks up the reads between the MFMAs and costs full tiles 5%).
+  auto pass = [&](bool stored) {
+    for_each_place<FM - 2>([&](auto place) {
+      fills(std::integral_constant<int, decltype(place)::value + 2>{}, filling);
+    });
+    advance();
+    if (stored) wait_vm<(NST - 2) * C::kPer + tile_stores<MODE, C, OUT>()>();
+    else wait_vm<(NST - 2) * C::kPer>();
+    join();
+    filling = slot;
+    fills(std::integral_constant<int, 0>{}, filling);
+    fills(std::integral_constant<int, 1>{}, filling);
+    slot = slot + 1 == NST ? 0 : slot + 1;
+  };
   for (int it = 0; it < n_items; ++it) {
-    step(std::integral_constant<bool, true>{}, it > 0);
-    for (int kt = 1; kt < nk; ++kt) step(std::integral_constant<bool, false>{}, false);
     const Item t = item_at(it);
+    if (C::WM > 1 && t.rows <= wm * 16 * FM) {
+      for (int kt = 0; kt < nk; ++kt) pass(it > 0 && kt == 0);
+      const uint32_t st = slot * C::kStage;
+      read_w(st);
+      read_x(st, 0, 0);
+      read_x(st, 1, 1);
+      take_w();
+    } else {
+      step(std::integral_constant<bool, true>{}, it > 0);
+      for (int kt = 1; kt < nk; ++kt) step(std::integral_constant<bool, false>{}, false);
+    }
     store_tile<MODE, C, OUT>(g, acc, t.m0, t.rows, t.n0);
   }
   wait_vm<0>();   // no fill may land after the workgroup's end
@@ -545,15 +571,22 @@ hipError_t run_rows(MxArgs g, const moe_dims& dm, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The large tile where there are full ones for most of the 256 CUs; else the
-// small one, whose workgroups are four times as many.
-bool use_big(const moe_dims& dm, int64_t cols) {
-  return dm.T * dm.k / Big::BM * ((cols + Big::BN - 1) / Big::BN) >= 256;
+// The large tile where the full ones would occupy half of the 256 CUs, the experts
+// have half a tile of rows each on average, and the K loop is long enough to hide
+// a tile's ends.  Both products, large against small tile, us, at d = 2048, f = 1024:
+//   8 experts of 256, 512 and 1024 rows: 49 and 42, 51 and 61, 89 and 92;
+//   256 experts of 32, 64, 128 and 256 rows: 253 and 232, 303 and 293, 370 and 417,
+//   534 and 683;
+// at d = f = 256, 16 experts of 512 and 4096 rows: 25 and 22, 47 and 40.
+bool use_big(const moe_dims& dm, int64_t cols, int64_t K) {
+  const int64_t R = dm.T * dm.k;
+  return R / Big::BM * ((cols + Big::BN - 1) / Big::BN) >= 128 && R >= 128 * dm.E && K >= 512;
 }
 
 }  // namespace
 
-// a launch holds fewer than 2^32 threads (dims this large take the big tile)
+// A launch holds fewer than 2^32 threads.  The large tile needs the most: up to four
+// times as many of the small one share their workgroups by kMaxItems, of half the threads.
 bool mx_tiles_ok(const moe_dims& dm) {
   const int64_t limit = (int64_t(1) << 32) / Big::NT;
   return grid_tiles<UP, Big>(dm, dm.f) < limit && grid_tiles<DOWN, Big>(dm, dm.d) < limit;
@@ -579,7 +612,7 @@ hipError_t launch_up_mx(const moe_dims& dm, const void* xq, const uint8_t* x_sca
   g.K = dm.d;
   g.N = dm.f;
   g.E = dm.E;
-  if (use_big(dm, 2 * static_cast<int64_t>(dm.f))) return run_rows<UP, Big, uint8_t>(g, dm, s);
+  if (use_big(dm, 2 * static_cast<int64_t>(dm.f), dm.d)) return run_rows<UP, Big, uint8_t>(g, dm, s);
   return run_rows<UP, Small, uint8_t>(g, dm, s);
 }
 
@@ -597,7 +630,7 @@ hipError_t launch_down_mx(const moe_dims& dm, const void* hq, const uint8_t* h_s
   g.K = dm.f;
   g.N = dm.d;
   g.E = dm.E;
-  const bool big = use_big(dm, dm.d);
+  const bool big = use_big(dm, dm.d, dm.f);
   if (dm.act == MOE_BF16)
     return big ? run_rows<DOWN, Big, bf16_t>(g, dm, s) : run_rows<DOWN, Small, bf16_t>(g, dm, s);
   return big ? run_rows<DOWN, Big, float>(g, dm, s) : run_rows<DOWN, Small, float>(g, dm, s);
