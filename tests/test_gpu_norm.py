@@ -191,6 +191,17 @@ def test_norm_backward(T, d, dtype, dsum):
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
 
 
+@pytest.mark.parametrize("T,d,dtype", [(523, 8256, torch.bfloat16), (523, 4160, torch.float32),
+                                       (129, 2112, torch.bfloat16), (513, 1024, torch.float32)])
+def test_norm_backward_of_several_rows_each(T, d, dtype):
+    """rows that take a workgroup, more of them than workgroups"""
+    print(f"\n[case] norm backward several rows {T}x{d} {dtype}", flush=True)
+    x, ds, w = _inputs(T, d, dtype, T + d, True)
+    dy = up(np.random.default_rng(d).normal(size=(T, d)), dtype)
+    dx, dw = _bwd(x, w, dy, ds)
+    _check_bwd(x, w, dy, ds, dx, dw)
+
+
 @pytest.mark.parametrize("d", [256, 4096, 20032])
 def test_norm_backward_in_place(d):
     print(f"\n[case] norm backward in place d={d}", flush=True)

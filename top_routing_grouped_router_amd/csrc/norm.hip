@@ -9,13 +9,12 @@
 //   n = s rstd;  g = dy w;  dx = rstd (g - n mean(g n)) + dsum;  dw = sum_t dy n
 //
 // Every pass is bound by HBM: each tensor is read and written once, with the
-// row held in registers between the sum of squares and the scaling.  A row
-// belongs to one wavefront where it fits its registers and there are rows
-// enough to fill the GPU (no barrier, no LDS), else to a workgroup of four
-// (fewer bytes per lane: a few rows are bound by latency, not bytes).  Rows
-// longer than a workgroup's registers are read twice.
+// row held in registers between the sum of squares and the scaling.  A short row
+// belongs to one wavefront (no barrier, no LDS), a longer one to a workgroup of
+// four (fewer bytes per lane, so more rows under way), and rows longer than a
+// workgroup's registers are read twice (kWavePieces).
 //
-// Measured: 16384 x 2048 bf16 with residual, y and 8-bit rows (303 MB) 55.5 us, 5.5
+// Measured: 16384 x 2048 bf16 with residual, y and 8-bit rows (303 MB) 52.5 us, 5.8
 // TB/s (a large copy reaches 5.2); forward and backward there (470 MB) 102 us, of which
 // 48, 51 and 4 for the weight gradient's second step; one row of 2048 2.5 us.
 #include <algorithm>
@@ -244,17 +243,21 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormBwdArgs a) {
   const int stream = threadIdx.x / L, lane = threadIdx.x % L, per_row = a.d / N;
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
   const int64_t r1 = min(r0 + a.chunk, a.T);
+  constexpr bool kKeep = NV <= 4;   // more pieces: the weight is read again (registers)
   float w[NV][N], dw[NV][N];
-#pragma unroll
-  for (int u = 0; u < NV; ++u) {
+  auto weights = [&](int u) {
     const int p = lane + u * L;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      dw[u][i] = 0.0f;
-      w[u][i] = p < per_row ? a.weight[p * N + i] : 0.0f;
-    }
+    for (int i = 0; i < N; ++i) w[u][i] = p < per_row ? a.weight[p * N + i] : 0.0f;
+  };
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) dw[u][i] = 0.0f;
+    if (kKeep) weights(u);
   }
   for (int64_t row = r0 + stream; row < r1; row += S) {
+    if (!kKeep) asm volatile("" ::: "memory");   // each row again, not kept
     uint4 dyv[NV], sv[NV], dsv[NV];
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
@@ -273,6 +276,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormBwdArgs a) {
       float dy[N], s[N];
       unpack16(dyv[u], dy, T{});
       unpack16(sv[u], s, T{});
+      if (!kKeep) weights(u);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float n = s[i] * rstd;
@@ -288,6 +292,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormBwdArgs a) {
       float gw[N], n[N];
       unpack16(dyv[u], gw, T{});
       unpack16(sv[u], n, T{});
+      if (!kKeep) weights(u);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         gw[i] *= w[u][i];
@@ -426,9 +431,13 @@ int pieces_per_lane(int pieces, int lanes) {
 // workgroups for `n` of rows: a launch holds fewer than 2^32 threads
 unsigned row_grid(int64_t n) { return static_cast<unsigned>(std::min<int64_t>(n, 1 << 23)); }
 
-// A wavefront per row from this many rows on (a wavefront for each of the 1024
-// SIMDs); below it the GPU is not full and a row's latency counts.
-constexpr int64_t kWaveRows = 1024;
+// Pieces of a row per lane up to which the row belongs to one wavefront.  us, bf16,
+// forward / backward, a wavefront and a workgroup to a row:
+//   2 pieces: 16384 x 1024 28.7 / 30.5 and 33.4 / 47.7, 64 x 1024 5.7 / 7.9 and 4.9 / 8.0;
+//   4 pieces: 16384 x 2048 55.8 / 58.3 and 53.1 / 59.0, 2048 x 2048 9.6 / 20.3 and 8.3 / 16.1.
+// Rows in registers against rows read twice: 16384 x 4096 96 / 109 and 124 / 161, 8 pieces
+// to a lane of a workgroup 16384 x 16384 455 / 503 and 491 / 671.
+constexpr int kWavePieces = 2;
 
 template <typename T, int W, int NV>
 hipError_t run_norm(const NormArgs& g, hipStream_t s) {
@@ -441,13 +450,8 @@ template <typename T>
 hipError_t norm(const NormArgs& g, hipStream_t s) {
   const int pieces = g.d / Act<T>::kPer16B;
   const int one = pieces_per_lane(pieces, 64), four = pieces_per_lane(pieces, 256);
-  if (one && one <= 4 && (g.T >= kWaveRows || one == 1)) {
-    switch (one) {
-      case 1: return run_norm<T, 1, 1>(g, s);
-      case 2: return run_norm<T, 1, 2>(g, s);
-      default: return run_norm<T, 1, 4>(g, s);
-    }
-  }
+  if (one && one <= kWavePieces)
+    return one == 1 ? run_norm<T, 1, 1>(g, s) : run_norm<T, 1, 2>(g, s);
   switch (four) {
     case 1: return run_norm<T, kWaves, 1>(g, s);
     case 2: return run_norm<T, kWaves, 2>(g, s);
@@ -469,16 +473,13 @@ template <typename T>
 hipError_t norm_bwd(const NormBwdArgs& a, int parts, hipStream_t s) {
   const int pieces = a.d / Act<T>::kPer16B;
   const int one = pieces_per_lane(pieces, 64), four = pieces_per_lane(pieces, 256);
-  if (one && one <= 4) {
-    switch (one) {
-      case 1: return run_norm_bwd<T, 1, 1>(a, parts, s);
-      case 2: return run_norm_bwd<T, 1, 2>(a, parts, s);
-      default: return run_norm_bwd<T, 1, 4>(a, parts, s);
-    }
-  }
-  switch (four) {   // rows of 4 or fewer pieces per lane; 2 is the least here
+  if (one && one <= kWavePieces)
+    return one == 1 ? run_norm_bwd<T, 1, 1>(a, parts, s) : run_norm_bwd<T, 1, 2>(a, parts, s);
+  switch (four) {
+    case 1: return run_norm_bwd<T, kWaves, 1>(a, parts, s);
     case 2: return run_norm_bwd<T, kWaves, 2>(a, parts, s);
     case 4: return run_norm_bwd<T, kWaves, 4>(a, parts, s);
+    case 8: return run_norm_bwd<T, kWaves, 8>(a, parts, s);
   }
   const unsigned cols = static_cast<unsigned>((pieces + kThreads - 1) / kThreads);
   hipLaunchKernelGGL((norm_dw_long_kernel<T>), dim3(parts, cols), dim3(kThreads), 0, s, a);
@@ -500,8 +501,15 @@ hipError_t launch_rmsnorm(const moe_dims& dm, const void* x, const void* res, co
 }
 
 // Workgroups of the backward pass: two for each of the 256 CUs, at least 4 rows each
+// (their weight gradients are read again), of rows that take a whole workgroup at
+// least one: 64 rows of 4096 in bf16 10.8 -> 7.5 us; a row each also where there are
+// 512 costs 12.0 -> 15.6.  At 16384 x 2048, 256 and 1024 workgroups take as long as 512
+// (58, 61 and 58 us), at 16384 x 512 longer (25, 20 and 19).
 int rmsnorm_bwd_parts(const moe_dims& dm) {
-  return static_cast<int>(std::min<int64_t>((dm.T + 3) / 4, 512));
+  const int pieces = dm.d / (dm.act == MOE_BF16 ? 8 : 4);
+  const int64_t few = pieces <= 64 * kWavePieces ? 1 : 128;
+  return static_cast<int>(
+      std::min(std::max((dm.T + 3) / 4, std::min(dm.T, few)), int64_t(512)));
 }
 
 hipError_t launch_rmsnorm_bwd(const moe_dims& dm, const void* dy, const void* s_in,
