@@ -616,6 +616,8 @@ moe_status moe_route_flips(int64_t T, int32_t k, int32_t E, const int32_t* topk_
  *   rows of `in` values.
  * moe_mx_dequantize: the values, rounded to dst_dtype (exact in bf16 but for
  *   its subnormal range and overflow), dst [rows, cols].
+ * Both: cols % 64 == 0 and rows * cols <= 2^35 (else MOE_ERR_UNSUPPORTED); the
+ *   tensors do not overlap.
  * moe_mx_scale_cols: [host] bytes of a scale row; 0 unless cols > 0 and
  *   cols % 64 == 0.
  */

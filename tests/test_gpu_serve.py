@@ -188,3 +188,17 @@ def test_layer_refuses_what_does_not_fit():
         M.moe_rmsnorm(dims, x[:8].bfloat16(), None, x[0], 1e-6, None, x[:8], None, None, None)
     with pytest.raises(ValueError, match="must be on"):
         M.moe_rmsnorm(dims, x[:8], None, x[0].cpu(), 1e-6, None, x[:8], None, None, None)
+
+
+def test_calls_refuse_other_devices_and_router_shapes():
+    serve = MoEServeLayer(8, 64, 4, 64, 2, torch.float32)
+    x = torch.zeros(8, 64, device="cuda")
+    with pytest.raises(ValueError, match="wr must be"):
+        serve.forward(x, x[0], x[:3])
+
+    class Elsewhere:   # a stream of another GPU
+        device_index, cuda_stream = torch.cuda.current_device() + 1, 0
+
+    with pytest.raises(ValueError, match="stream must be on"):
+        M.moe_rmsnorm(M.make_dims(8, 64, 4, 64, 2, torch.float32), x, None, x[0], 1e-6, None, x,
+                      None, None, None, stream=Elsewhere())

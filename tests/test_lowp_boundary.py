@@ -103,6 +103,16 @@ def test_mx_arguments():
     assert quant(src=None)[0] == INVALID and dequant(dst=None)[0] == INVALID
 
 
+def test_mx_sizes_end_where_a_launch_does():
+    """2^35 values of 4 bytes are 2^31 threads of 4 pieces; one row more is refused"""
+    rows = (1 << 35) // 64 + 1
+    for cols, dt in ((64, 0), (64, 1)):
+        for fn, args in (("moe_mx_quantize", (dt, FAKE, 0)), ("moe_mx_dequantize", (0, FAKE, FAKE))):
+            tail = (FAKE, FAKE, None) if fn == "moe_mx_quantize" else (dt, FAKE, None)
+            st, why = call(fn, rows, cols, *args, *tail)
+            assert st == UNSUP and "2^35" in why
+
+
 def test_experts_arguments():
     for at in range(10):
         p = [FAKE] * 10

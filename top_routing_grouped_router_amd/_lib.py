@@ -692,8 +692,12 @@ def _workspace(t, device):
 
 def _enqueue(func, device, stream, *args):
     """Runs an entry point on GPU `device`: on its current stream unless one is given."""
-    raw = (torch._C._cuda_getCurrentRawStream(device) if stream is None   # 2 us less than
-           else stream.cuda_stream)                                       # current_stream()
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device)   # 2 us less than current_stream()
+    else:
+        if stream.device_index != device:
+            raise ValueError(f"stream must be on cuda:{device}, is on cuda:{stream.device_index}")
+        raw = stream.cuda_stream
     fn = getattr(lib(), func)
     if device == torch.cuda.current_device():
         st = fn(*args, raw)

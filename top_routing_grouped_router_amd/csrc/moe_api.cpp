@@ -351,8 +351,8 @@ moe_status check_mx_rows(int64_t rows, int32_t cols, int32_t dtype, int32_t form
     return fail(MOE_ERR_INVALID_ARGUMENT, "%s: need rows >= 0 and cols > 0 (rows=%lld cols=%d)", fn,
                 static_cast<long long>(rows), cols);
   if (cols % 64) return fail(MOE_ERR_UNSUPPORTED, "%s: cols=%d must be a multiple of 64", fn, cols);
-  if (rows > (int64_t(1) << 36) / cols)
-    return fail(MOE_ERR_UNSUPPORTED, "%s: rows*cols must be at most 2^36", fn);
+  if (rows > (int64_t(1) << 35) / cols)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: rows*cols must be at most 2^35", fn);
   if (dtype != MOE_F32 && dtype != MOE_BF16)
     return fail(MOE_ERR_UNSUPPORTED, "%s: dtype=%d is neither MOE_F32 nor MOE_BF16", fn, dtype);
   if (format != MOE_MX_E4M3 && format != MOE_MX_E2M1)

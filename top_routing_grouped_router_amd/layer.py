@@ -187,6 +187,10 @@ class MoELayer:
         if self.pre_norm != (norm_weight is not None) or (residual is not None
                                                           and not self.pre_norm):
             raise ValueError("norm_weight goes with pre_norm=True, and so does residual")
+        with torch.cuda.device_of(x):
+            return self._forward(x, wr, w1, w3, w2, routing, norm_weight, residual)
+
+    def _forward(self, x, wr, w1, w3, w2, routing, norm_weight, residual):
         if self.pre_norm:
             x = self.norm(x, norm_weight, residual)
         self.route(x, wr)
@@ -204,13 +208,14 @@ class MoELayer:
         reaches `stream` from elsewhere."""
         if self.pre_norm != (norm_weight is not None) or (dsum is not None and not self.pre_norm):
             raise ValueError("norm_weight goes with pre_norm=True, and so does dsum")
-        if not self.pre_norm:
-            return self._layer_bwd(dy, x, wr, w1, w3, w2)
-        if self.stream is None:
+        if self.pre_norm and self.stream is None:
             raise ValueError("backward before forward")
-        self._layer_bwd(dy, self.xn, wr, w1, w3, w2)
-        L.moe_rmsnorm_bwd(self.dims, self.dx, self.stream, norm_weight, self.rstd, dsum,
-                          self.dstream, self.dnorm, self.workspace)
+        with torch.cuda.device_of(dy):
+            if not self.pre_norm:
+                return self._layer_bwd(dy, x, wr, w1, w3, w2)
+            self._layer_bwd(dy, self.xn, wr, w1, w3, w2)
+            L.moe_rmsnorm_bwd(self.dims, self.dx, self.stream, norm_weight, self.rstd, dsum,
+                              self.dstream, self.dnorm, self.workspace)
         return self.dstream
 
     def _layer_bwd(self, dy, x, wr, w1, w3, w2):
@@ -274,7 +279,8 @@ class MoEServeLayer:
 
     Up to few_slots token-expert pairs go through moe_token_swiglu (activations
     in `act`, nothing sorted), more through the grouped products on 8-bit rows.
-    The outputs are buffers that the next forward overwrites.
+    The outputs are buffers that the next forward overwrites: one forward at a time,
+    on one stream or with its own ordering between them.
     """
 
     def __init__(self, max_tokens: int, d: int, E: int, f: int, k: int, act: torch.dtype,
@@ -325,6 +331,12 @@ class MoEServeLayer:
         T = x.shape[0]
         if x.dim() != 2 or x.shape[1] != self.d or T > self.T:
             raise ValueError(f"x must be [T, {self.d}] with T <= {self.T}, is {tuple(x.shape)}")
+        if tuple(wr.shape) != (self.E, self.d):
+            raise ValueError(f"wr must be [{self.E}, {self.d}], is {tuple(wr.shape)}")
+        with torch.cuda.device_of(x):
+            return self._forward(x, norm_weight, wr, residual, T)
+
+    def _forward(self, x, norm_weight, wr, residual, T):
         R = T * self.k
         dims, few = self._dims(T), R <= self.few_slots
         stream = x if residual is None else self.norm_sum[:T]
