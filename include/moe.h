@@ -633,13 +633,13 @@ moe_status moe_mx_dequantize(int64_t rows, int32_t cols, int32_t format, const v
  *
  *   s[t] = x[t] + residual[t], rounded to act;
  *   rstd[t] = 1 / sqrt(mean(s[t]^2) + eps);  y[t] = s[t] rstd[t] weight.
- * The norm is of s as stored.  Squares and sums are fp32 (an |s| above about
- * 1e19 overflows them: rstd 0).
+ * The norm is of s as stored.  Squares are fp32 (an |s| above about 1e19
+ * overflows them: rstd 0).
  * x [T,d] act; residual [T,d] act or NULL (s = x); weight [d] fp32; eps >= 0.
  * sum [T,d] act or NULL: s.  It may be x or residual (in place).
  * y [T,d] act or NULL; it may be x when sum is not.
  * q [T,d] E4M3 and q_scale [T, moe_mx_scale_cols(d)], both or neither: the
- *   fp32 y, quantised (not its act rounding).  y or q has to be given.
+ *   y before its rounding to act, quantised.  y or q has to be given.
  * rstd [T] fp32 or NULL (the backward pass reads it).
  * Of dims, only T, d and act matter (E, f, k have to be valid).
  *

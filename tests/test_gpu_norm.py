@@ -91,6 +91,35 @@ def test_norm(T, d, dtype, res):
     _check(x, r, w, _run(x, r, w, total=res))
 
 
+@pytest.mark.parametrize("T,d", [(1, 64), (3, 320), (2, 2048), (2, 16448), (2, 40000)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_elements_next_to_ties(T, d, dtype):
+    """rows of small integers, whose squares add up exactly, and a weight that puts every
+    y of the first row within a rounding of a tie between elements, or of its scale's
+    limit: each element is still the rounding of y.  rstd is good to 2^-45, y to
+    2^-43, and the closest y lies further from its tie than that (checked)."""
+    d = d // 64 * 64
+    print(f"\n[case] norm ties {T}x{d} {dtype}", flush=True)
+    rng = np.random.default_rng(d)
+    s = rng.integers(1, 12, size=(T, d)) * rng.choice([-1, 1], size=(T, d))
+    tie = (8 + rng.integers(0, 8, size=d) + 0.5) / 8 * 2.0 ** rng.integers(-3, 8, size=d)
+    tie[::32] = rng.choice([448.0, 400.0], size=d // 32)
+    tie[tie > 448] = 232.0
+    rstd = 1 / np.sqrt(np.mean(s[0] * s[0]) + float(np.float32(EPS)))
+    w = up(tie / (np.abs(s[0]) * rstd), torch.float32)
+    x = up(s, dtype)
+    y, _ = O.rmsnorm(s, host64(w), float(np.float32(EPS)))
+    off = np.abs(np.abs(y[0]) / tie - 1)
+    assert (off <= 2.0 ** -24).all() and (off > 2.0 ** -42).all()
+    o = _run(x, None, w, total=False)
+    want, scale = O.mx_quantize(y, "e4m3")
+    got_s = o["scale"].cpu().numpy()
+    assert (got_s[:, :d // 32] == scale).all()
+    v = O.mx_element_values(o["q"].cpu().numpy(), "e4m3")
+    bad = np.argwhere(v != want)
+    assert not len(bad), (len(bad), bad[:5], v[tuple(bad[0])], want[tuple(bad[0])])
+
+
 @pytest.mark.parametrize("dtype,d", [(torch.float32, 64), (torch.bfloat16, 64), (torch.float32, 320),
                                      (torch.bfloat16, 448), (torch.float32, 1024),
                                      (torch.bfloat16, 2048), (torch.bfloat16, 2112)])

@@ -4,8 +4,11 @@
 //   s = round(x + r);  rstd = 1 / sqrt(mean(s^2) + eps);  y = (s rstd) w
 // The norm is taken of s as it is stored (rounded to the act type), so the
 // backward pass, which reads s, differentiates what the forward computed.
-// Squares, means and products are fp32; y is rounded once, and the 8-bit rows
-// come from the fp32 y, not from its rounding.
+// Squares are summed in fp32 by fours and those sums in 64 bits (an addition per four
+// values), y is an fp32 product rounded once to the act type, and the 8-bit rows are
+// the roundings of y itself, not of that product: near ties it is computed again with
+// what its roundings lost (16384 x 2048 rows: no element off instead of 24; 55.0 us
+// instead of 52.5, and 57.1 with every element computed so).
 //   n = s rstd;  g = dy w;  dx = rstd (g - n mean(g n)) + dsum;  dw = sum_t dy n
 //
 // Every pass is bound by HBM: each tensor is read and written once, with the
@@ -14,8 +17,8 @@
 // four (fewer bytes per lane, so more rows under way), and rows longer than a
 // workgroup's registers are read twice (kWavePieces).
 //
-// Measured: 16384 x 2048 bf16 with residual, y and 8-bit rows (303 MB) 52.5 us, 5.8
-// TB/s (a large copy reaches 5.2); forward and backward there (470 MB) 102 us, of which
+// Measured: 16384 x 2048 bf16 with residual, y and 8-bit rows (303 MB) 55.0 us, 5.5
+// TB/s (a large copy reaches 5.2); forward and backward there (470 MB) 103 us, of which
 // 48, 51 and 4 for the weight gradient's second step; one row of 2048 2.5 us.
 #include <algorithm>
 
@@ -27,7 +30,8 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 
-__device__ __forceinline__ float wave_sum(float v) {
+template <typename F>
+__device__ __forceinline__ F wave_sum(F v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
   return v;
@@ -35,11 +39,11 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 // sum over the W wavefronts of a row (W = 1: the wavefront's own), the same in
 // every lane.  The caller's loop may come here again at once: two barriers.
-template <int W>
-__device__ __forceinline__ float row_sum(float v) {
+template <int W, typename F>
+__device__ __forceinline__ F row_sum(F v) {
   v = wave_sum(v);
   if constexpr (W > 1) {
-    __shared__ float part[W];
+    __shared__ F part[W];
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
     v = part[0];
@@ -50,12 +54,44 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// sum of N squares by halves: the error of a long row's sum, which shifts every
-// 8-bit rounding of the row, grows with the depth of the tree
+// sum += N squares: four at a time in fp32, whose error is a fraction of 2^-24 of the
+// whole row's sum
 template <int N>
-__device__ __forceinline__ float squares(const float* v) {
-  if constexpr (N == 1) return v[0] * v[0];
-  else return squares<N / 2>(v) + squares<N / 2>(v + N / 2);
+__device__ __forceinline__ double squares(const float* v, double sum) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4)
+    sum += (v[i] * v[i] + v[i + 1] * v[i + 1]) + (v[i + 2] * v[i + 2] + v[i + 3] * v[i + 3]);
+  return sum;
+}
+
+// 1 / sqrt(m) as the sum of two floats: the instruction's estimate (about 24 bits) and
+// a step of Newton's method, which doubles them
+struct Rstd {
+  float hi, lo;
+};
+__device__ __forceinline__ Rstd inverse_root(double m) {
+  double r = __builtin_amdgcn_rsq(m);
+  if (m > 0.0 && m < HUGE_VAL) r = fma(r, 0.5 * fma(-m * r, r, 1.0), r);
+  Rstd out;
+  out.hi = static_cast<float>(r);
+  out.lo = static_cast<float>(r - out.hi);
+  return out;
+}
+
+// The 8-bit rows are the roundings of y itself.  v = fl(fl(s rstd.hi) w) is within
+// 3 * 2^-24 |y| of it, at most 3 of its last places, so only a v that close to a tie
+// between elements, or to a scale's limit, can round to another element; these all
+// have 19 zero bits behind the first four of the significand.
+constexpr uint32_t kTieBits = 0x7FFFF, kTieNear = 4;
+// y for those: to about 2^-45, rounded to odd, so that any later rounding to fewer
+// bits is that of the sum itself
+__device__ __forceinline__ float scaled_odd(float s, Rstd r, float w) {
+  const float n = s * r.hi, en = fmaf(s, r.lo, fmaf(s, r.hi, -n));
+  const float y = n * w, ey = fmaf(en, w, fmaf(n, w, -y));
+  const float hi = y + ey, lo = (y - hi) + ey;
+  const uint32_t u = __float_as_uint(hi);
+  const int away = static_cast<int>(u ^ __float_as_uint(lo)) < 0 ? -1 : 1;
+  return __uint_as_float(lo != 0.0f && !(u & 1) ? u + away : u);
 }
 
 struct NormArgs {
@@ -70,6 +106,7 @@ struct NormArgs {
   int64_t T;
   int d;
   float eps;
+  double inv_d;   // 1 / d
 };
 
 // a 16-byte piece: one that is read once goes past the caches' retention (with the
@@ -104,20 +141,25 @@ __device__ __forceinline__ void piece_sum(const NormArgs& g, int64_t at, uint4 x
 // y of one piece from s: the act row, the 8-bit row and its scales
 template <typename T>
 __device__ __forceinline__ void piece_out(const NormArgs& g, int64_t row, int p, int per_row,
-                                          float rstd, const float* s) {
+                                          Rstd rstd, const float* s) {
   constexpr int N = Act<T>::kPer16B;
   constexpr int kLanes = 32 / N;
-  float v[N];
+  float v[N], w[N];
 #pragma unroll
-  for (int i = 0; i < N / 4; ++i) {
-    const float4 w = reinterpret_cast<const float4*>(g.weight)[p * (N / 4) + i];
-    v[4 * i] = s[4 * i] * rstd * w.x;
-    v[4 * i + 1] = s[4 * i + 1] * rstd * w.y;
-    v[4 * i + 2] = s[4 * i + 2] * rstd * w.z;
-    v[4 * i + 3] = s[4 * i + 3] * rstd * w.w;
-  }
+  for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(w + i) =
+      reinterpret_cast<const float4*>(g.weight)[p * (N / 4) + i / 4];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = s[i] * rstd.hi * w[i];
   if (g.y) st_nt16(reinterpret_cast<uint4*>(g.y) + row * per_row + p, pack16(v, T{}));
   if (g.q) {
+    uint32_t least = kTieBits;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      least = min(least, (__float_as_uint(v[i]) + kTieNear) & kTieBits);
+    if (least <= 2 * kTieNear) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = scaled_odd(s[i], rstd, w[i]);
+    }
     const uint32_t sb = mx_store<kE4M3, N>(v, g.q + (row * per_row + p) * N);
     if (p % kLanes == 0) {
       const int ld = mx_scale_ld(g.d), b = p / kLanes;
@@ -149,17 +191,18 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs g) {
         if (g.res) rv[u] = load16(g.res, row * per_row + p);
       }
     }
-    float s[NV][N], ss = 0.0f;
+    float s[NV][N];
+    double ss = 0.0;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       const int p = lane + u * L;
       if (p < per_row) {
         piece_sum<T>(g, row * per_row + p, xv[u], rv[u], s[u]);
-        ss += squares<N>(s[u]);
+        ss = squares<N>(s[u], ss);
       }
     }
-    const float rstd = 1.0f / sqrtf(row_sum<W>(ss) / static_cast<float>(g.d) + g.eps);
-    if (g.rstd && lane == 0) g.rstd[row] = rstd;
+    const Rstd rstd = inverse_root(row_sum<W>(ss) * g.inv_d + g.eps);
+    if (g.rstd && lane == 0) g.rstd[row] = rstd.hi;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       const int p = lane + u * L;
@@ -181,16 +224,16 @@ __global__ __launch_bounds__(kThreads) void norm_long_kernel(NormArgs g) {
     again.res = nullptr;
   }
   for (int64_t row = blockIdx.x; row < g.T; row += gridDim.x) {
-    float ss = 0.0f;
+    double ss = 0.0;
     for (int p = threadIdx.x; p < per_row; p += kThreads) {
       float s[N];
       const int64_t at = row * per_row + p;
       piece_sum<T>(g, at, load16_kept(g.x, at),
                    g.res ? load16_kept(g.res, at) : make_uint4(0, 0, 0, 0), s);
-      ss += squares<N>(s);
+      ss = squares<N>(s, ss);
     }
-    const float rstd = 1.0f / sqrtf(row_sum<kWaves>(ss) / static_cast<float>(g.d) + g.eps);
-    if (g.rstd && threadIdx.x == 0) g.rstd[row] = rstd;
+    const Rstd rstd = inverse_root(row_sum<kWaves>(ss) * g.inv_d + g.eps);
+    if (g.rstd && threadIdx.x == 0) g.rstd[row] = rstd.hi;
     for (int p = threadIdx.x; p < per_row; p += kThreads) {
       float s[N];
       const int64_t at = row * per_row + p;
@@ -496,7 +539,8 @@ hipError_t launch_rmsnorm(const moe_dims& dm, const void* x, const void* res, co
                           float eps, void* sum, void* y, void* q, uint8_t* q_scale, float* rstd,
                           hipStream_t s) {
   if (dm.T == 0) return hipSuccess;
-  NormArgs g{x, res, weight, sum, y, static_cast<uint8_t*>(q), q_scale, rstd, dm.T, dm.d, eps};
+  NormArgs g{x, res, weight, sum, y, static_cast<uint8_t*>(q), q_scale, rstd, dm.T, dm.d, eps,
+             1.0 / dm.d};
   return dm.act == MOE_BF16 ? norm<bf16_t>(g, s) : norm<float>(g, s);
 }
 
