@@ -149,6 +149,39 @@ def test_large_tiles_of_few_rows(T, d, E, f, gather):
     c.check()
 
 
+@pytest.mark.parametrize("act", [torch.bfloat16, torch.float32])
+def test_the_down_products_tiles_agree(act):
+    """a batch with eight large tiles to a workgroup gives each expert's rows the bits
+    that batches of a few tiles give them; rows behind the last expert stay"""
+    print(f"\n[case] experts_mx down tiles {act}", flush=True)
+    T, d, E, f, k = 16640, 4160, 6, 576, 2
+    counts = [129, 16000, 0, 1, 17020, 100]
+    off = np.r_[0, np.cumsum(counts)]
+    n = int(off[-1])
+    gen = torch.Generator(device="cuda").manual_seed(5)
+
+    def codes(*shape, top=256):
+        return torch.randint(0, top, shape, dtype=torch.uint8, device="cuda", generator=gen)
+
+    hq = codes(T * k, f)
+    hq[(hq & 127) == 127] = 3                                   # no NaN
+    hs = codes(T * k, O.mx_scale_cols(f), top=9) + 120
+    w2, ws = codes(E, d, f // 2), codes(E, d, O.mx_scale_cols(f), top=9) + 120
+    y = torch.full((T * k, d), float("nan"), dtype=act, device="cuda")
+    M.moe_expert_down_mx(M.make_dims(T, d, E, f, k, act), hq, hs,
+                         torch.tensor(off, dtype=torch.int32, device="cuda"), w2, ws, y)
+    assert torch.isnan(y[n:]).all() and torch.isfinite(y[:n]).all()
+    for e in range(E):
+        for a in range(int(off[e]), int(off[e + 1]), 4096):
+            b = min(a + 4096, int(off[e + 1]))
+            part = torch.empty(b - a, d, dtype=act, device="cuda")
+            M.moe_expert_down_mx(M.make_dims(b - a, d, 1, f, 1, act), hq[a:b].clone(),
+                                 hs[a:b].clone(),
+                                 torch.tensor([0, b - a], dtype=torch.int32, device="cuda"),
+                                 w2[e:e + 1], ws[e:e + 1], part)
+            assert torch.equal(y[a:b], part), (e, a)
+
+
 def test_rows_without_a_table():
     print("\n[case] experts_mx no table", flush=True)
     c = Case(50, 192, 3, 128, 2, [40, 0, 60], torch.bfloat16, seed=1, gather=False)

@@ -31,14 +31,16 @@
 //
 // Measured at 98304 rows, d = 2048, 64 experts of 1024 (UP and DOWN together,
 // 1.24 TFLOP): one tile per workgroup 709 us; the persistent stream of tiles 650;
-// fills spread between the MFMAs instead of all behind the barrier 612, and without
-// the MFMAs of wavefronts past a tile's rows 608.  Without
-// the epilogues (the exponential and reciprocal of silu, at a quarter of the
-// vector rate, while the matrix cores idle) the same loop takes about 100 us
-// less, without the fills 85 less (the scales' words, one line a row, are half
-// of the lines fetched), and without both and the barriers 390: the rate of the
-// MFMAs at the power limit.  Two workgroups to a CU with 128 x 256 tiles hide the
-// epilogues but fill a third more: 664.
+// fills spread between the MFMAs instead of all behind the barrier 612; without the
+// MFMAs of wavefronts past a tile's rows 608; DOWN by wavefronts of 128 x 128, 588
+// (360 and 233 by themselves).  The MFMAs alone are 257 us at 2.4 GHz and about 300
+// at the clock that random data leaves.  What the rest is, by leaving out parts of the
+// loop: DOWN's 402 MB of stores cost it 75 us, UP's epilogue (the exponential and
+// reciprocal of silu, at a quarter of the vector rate, while the matrix cores idle)
+// 45, all fills 20 to 40 a product, barriers 10 to 25.  Two workgroups to a CU with
+// 128 x 256 tiles hide the epilogues but fill a third more: 664.  An epilogue spread
+// over the next tile's first step, fills sent ahead of the stores, stores past the
+// caches' retention and starts staggered over the CUs change nothing or lose.
 #include <algorithm>
 #include <type_traits>
 
@@ -112,12 +114,12 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
 }
 
-// Tile configurations: WM x WN wavefronts of FM x 4 fragments of 16 x 16, a ring
+// Tile configurations: WM x WN wavefronts of FM x FN fragments of 16 x 16, a ring
 // of NST stages, PER_CU workgroups resident on a CU.
-template <int FM_, int WM_, int WN_, int NST_, int PER_CU_>
+template <int FM_, int FN_, int WM_, int WN_, int NST_, int PER_CU_>
 struct Tile {
-  static constexpr int FM = FM_, WM = WM_, WN = WN_, NST = NST_, PER_CU = PER_CU_;
-  static constexpr int BM = 16 * FM * WM, BN = 64 * WN;
+  static constexpr int FM = FM_, FN = FN_, WM = WM_, WN = WN_, NST = NST_, PER_CU = PER_CU_;
+  static constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
   static constexpr int NW = WM * WN, NT = 64 * NW;
   static constexpr int kA = BM * kStep, kB = BN * kStep / 2, kS = (BM + BN) * 4;
   static constexpr int kStage = kA + kB + kS;
@@ -126,16 +128,28 @@ struct Tile {
   static constexpr int PS = ((BM + BN) / 64 + NW - 1) / NW;     // and 64 words of scales
   static constexpr int kPer = PA + PB + PS;
   static_assert(BM % (8 * NW) == 0 && BN % (16 * NW) == 0 && (BM + BN) % 64 == 0, "whole fills");
-  static_assert(FM % 4 == 0, "a ring of four row fragments");
+  static_assert(FM % FN == 0, "a ring of FN row fragments");
   static_assert(NST >= 3, "a stage on its way while the next one is waited for");
 };
-typedef Tile<8, 2, 4, 3, 1> Big;     // 256 x 256
-typedef Tile<4, 1, 4, 3, 2> Small;   // 64 x 256
+typedef Tile<8, 4, 2, 4, 3, 1> Big;     // 256 x 256, wavefronts of 128 x 64
+typedef Tile<8, 8, 2, 2, 3, 1> Wide;    // 256 x 256, wavefronts of 128 x 128
+typedef Tile<4, 4, 1, 4, 3, 2> Small;   // 64 x 256
+
+// The accumulators of a row fragment stand in registers here, in order with what is
+// volatile around: 256 of them in the accumulation registers, fewer in the others.
+template <int FN>
+__device__ __forceinline__ void pin(f32x4 (&acc)[FN]) {
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    if constexpr (FN > 4) asm volatile("" : "+a"(acc[j]));
+    else asm volatile("" : "+v"(acc[j]));
+  }
+}
 
 // stores of a wavefront for one tile (store_tile)
 template <int MODE, typename C, typename OUT>
 constexpr int tile_stores() {
-  return MODE == UP ? 2 * C::FM : C::FM * static_cast<int>(sizeof(OUT));
+  return MODE == UP ? 2 * C::FM : C::FM * C::FN * static_cast<int>(sizeof(OUT)) / 4;
 }
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
@@ -152,26 +166,23 @@ __device__ __forceinline__ uint32_t max_over_groups(uint32_t v) {
   return max(b[0], b[1]);
 }
 
-// Which weight row of a wavefront's columns lane r of column fragment j holds:
-// chosen so that a lane's outputs over its fragments lie side by side (UP: 8
-// columns of a and the same of b; DOWN: 16).
-template <int MODE>
+// Which weight row of a wavefront's columns lane r of column fragment j holds: chosen
+// so that a lane's outputs of two fragments lie side by side, 8 columns, and those of
+// its four lane groups too (UP: two fragments of a and the same of b; DOWN: 64 columns).
 __device__ __forceinline__ int frag_col(int r, int j) {
-  return MODE == UP ? 8 * (r >> 2) + 4 * j + (r & 3) : 16 * (r >> 2) + 4 * j + (r & 3);
+  return 32 * (j >> 1) + 8 * (r >> 2) + 4 * (j & 1) + (r & 3);
 }
 // chunk swizzle of weight row n: distinct for the four runs of a fragment
-template <int MODE>
-__device__ __forceinline__ int w_key(int n) {
-  return (n >> (MODE == UP ? 3 : 4)) & 3;
-}
+__device__ __forceinline__ int w_key(int n) { return (n >> 3) & 3; }
 
 // The tile's outputs, from registers: lane (r, q) holds row r of each row
-// fragment, and of the wavefront's columns 8 q + [0, 8) (UP) or 16 q + [0, 16).
+// fragment, and of the wavefront's columns 8 q + [0, 8), DOWN also 32 + 8 q + [0, 8).
 // Rows and columns out of range are dropped by the buffer bounds, so every
 // wavefront issues the same number of stores, which the fill counts allow for.
 template <int MODE, typename C, typename OUT>
-__device__ __forceinline__ void store_tile(const MxArgs& g, const f32x4 (&acc)[C::FM][4], int m0,
-                                           int rows, int n0) {
+__device__ __forceinline__ void store_tile(const MxArgs& g, f32x4 (&acc)[C::FM][C::FN],
+                                           int m0, int rows, int n0) {
+  constexpr int FN = C::FN;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WN, wn = wave % C::WN;
   int lane = threadIdx.x & 63;
@@ -183,8 +194,10 @@ __device__ __forceinline__ void store_tile(const MxArgs& g, const f32x4 (&acc)[C
 #pragma unroll
   for (int i = 0; i < C::FM; ++i) {
     __builtin_amdgcn_sched_barrier(0);   // one row fragment's temporaries at a time
+    pin<FN>(acc[i]);
     const int row = wm * 16 * C::FM + i * 16 + r;
     if constexpr (MODE == UP) {
+      static_assert(FN == 4, "a block of h from two fragments of a and two of b");
       float h[8];
       uint32_t amax = 0;
 #pragma unroll
@@ -208,21 +221,25 @@ __device__ __forceinline__ void store_tile(const MxArgs& g, const f32x4 (&acc)[C
           static_cast<int>(row < rows && q == 0 && n / 32 < ldn
                                ? static_cast<uint32_t>(row) * ldn + n / 32 : kOutOfRange), 0, 0);
     } else {
-      const int n = n0 + wn * 64;
-      const uint32_t at = (static_cast<uint32_t>(row) * N + n + q * 16) * sizeof(OUT);
-      const bool in = row < rows && n < N;
-      if constexpr (sizeof(OUT) == 2) {
 #pragma unroll
-        for (int j = 0; j < 4; j += 2)
-          store16(out, in ? at + j * 8 : kOutOfRange,
-                  u32x4{bf16x2_rne(acc[i][j][0], acc[i][j][1]),
-                        bf16x2_rne(acc[i][j][2], acc[i][j][3]),
-                        bf16x2_rne(acc[i][j + 1][0], acc[i][j + 1][1]),
-                        bf16x2_rne(acc[i][j + 1][2], acc[i][j + 1][3])});
-      } else {
+      for (int b = 0; b < FN / 4; ++b) {   // 64 columns
+        const int n = n0 + wn * 16 * FN + 64 * b;
+        const uint32_t at = (static_cast<uint32_t>(row) * N + n + q * 8) * sizeof(OUT);
+        const bool in = row < rows && n < N;
+        const f32x4* a = acc[i] + 4 * b;
+        if constexpr (sizeof(OUT) == 2) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          store16(out, in ? at + j * 16 : kOutOfRange, __builtin_bit_cast(u32x4, acc[i][j]));
+          for (int j = 0; j < 4; j += 2)
+            store16(out, in ? at + frag_col(0, j) * 2 : kOutOfRange,
+                    u32x4{bf16x2_rne(a[j][0], a[j][1]), bf16x2_rne(a[j][2], a[j][3]),
+                          bf16x2_rne(a[j + 1][0], a[j + 1][1]),
+                          bf16x2_rne(a[j + 1][2], a[j + 1][3])});
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            store16(out, in ? at + frag_col(0, j) * 4 : kOutOfRange,
+                    __builtin_bit_cast(u32x4, a[j]));
+        }
       }
     }
   }
@@ -239,8 +256,8 @@ __device__ __forceinline__ void for_each_place(F&& f) {
 // of K steps, so the fills of a tile's first steps are on their way while the
 // last one is multiplied and stored.
 template <int MODE, typename C, typename OUT>
-__global__ __launch_bounds__(C::NT, C::PER_CU * C::NW / 4) void mx_rows_kernel(MxArgs g) {
-  constexpr int FM = C::FM, NST = C::NST, BM = C::BM, BN = C::BN, NW = C::NW;
+__global__ __launch_bounds__(C::NT, (C::PER_CU * C::NW + 3) / 4) void mx_rows_kernel(MxArgs g) {
+  constexpr int FM = C::FM, FN = C::FN, NST = C::NST, BM = C::BM, BN = C::BN, NW = C::NW;
   constexpr int kRing = C::kStage * NST;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kRing];
   __shared__ __attribute__((aligned(16))) int4 s_desc[kMaxItems];
@@ -288,7 +305,7 @@ __global__ __launch_bounds__(C::NT, C::PER_CU * C::NW / 4) void mx_rows_kernel(M
 #pragma unroll
   for (int u = 0; u < C::PB; ++u) {
     const int row = (wave * C::PB + u) * 16 + (lane >> 2);
-    last_b |= (((lane & 3) ^ w_key<MODE>(row)) >= 2 ? 1u : 0u) << u;
+    last_b |= (((lane & 3) ^ w_key(row)) >= 2 ? 1u : 0u) << u;
   }
   const bool second = MODE == UP && wave * C::PB * 16 >= kCols;   // this wavefront fills W3
   const uint8_t *abase = g.a, *bbase = g.w0, *sbase[C::PS];
@@ -325,7 +342,7 @@ __global__ __launch_bounds__(C::NT, C::PER_CU * C::NW / 4) void mx_rows_kernel(M
 #pragma unroll
     for (int u = 0; u < C::PB; ++u) {
       const int row = (wave * C::PB + u) * 16 + (lane >> 2);
-      const int chunk = (lane & 3) ^ w_key<MODE>(row);
+      const int chunk = (lane & 3) ^ w_key(row);
       const int n = row & (kCols - 1);
       vb[u] = t.n0 + n < N ? static_cast<uint32_t>(n) * (K / 2) + chunk * 16 : kOutOfRange;
     }
@@ -395,57 +412,58 @@ __global__ __launch_bounds__(C::NT, C::PER_CU * C::NW / 4) void mx_rows_kernel(M
   // ---- fragments
   const int wm = wave / C::WN, wn = wave % C::WN;
   const int r = lane & 15, q = lane >> 4;
-  f32x4 acc[FM][4];
-  constexpr int kFragW = MODE == UP ? 2 : 4;   // column fragments of one matrix
-  const int wcol = wn * 16 * kFragW + frag_col<MODE>(r, 0);
+  f32x4 acc[FM][FN];
+  constexpr int kFragW = MODE == UP ? FN / 2 : FN;   // column fragments of one matrix
+  const int wcol = wn * 16 * kFragW + frag_col(r, 0);
   const uint32_t aoff0 = (wm * 16 * FM + r) * kStep + ((q ^ ((r >> 1) & 7)) * 16);
   const uint32_t aoff1 = (wm * 16 * FM + r) * kStep + (((4 + q) ^ ((r >> 1) & 7)) * 16);
-  const uint32_t boff = C::kA + wcol * (kStep / 2) + ((q ^ w_key<MODE>(wcol)) * 16);
+  const uint32_t boff = C::kA + wcol * (kStep / 2) + ((q ^ w_key(wcol)) * 16);
   const uint32_t sxoff = C::kA + C::kB + (wm * 16 * FM + r) * 4;
   const uint32_t swoff = C::kA + C::kB + (BM + wcol) * 4;
-  // Row fragments go through a ring of four, read two ahead of their MFMAs; the
+  // Row fragments go through a ring of FN, read FN / 2 ahead of their MFMAs; the
   // column fragments of the next step are read beside the last row fragments.
-  i32x8 x[4];
-  int sx[4];
-  i32x4 w[4], w_next[4];
-  int sw[4], sw_next[4];
-  auto read_x = [&](uint32_t st, int i, int to) {
+  constexpr int P = FN / 2;   // row fragments behind a step's join
+  i32x8 x[FN];
+  int sx[FN];
+  i32x4 w[FN], w_next[FN];
+  int sw[FN], sw_next[FN];
+  auto read_x = [&](uint32_t st, int i) {
     const i32x4 lo = *reinterpret_cast<const i32x4*>(lds + st + aoff0 + i * 16 * kStep);
     const i32x4 hi = *reinterpret_cast<const i32x4*>(lds + st + aoff1 + i * 16 * kStep);
-    x[to] = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    sx[to] = *reinterpret_cast<const int*>(lds + st + sxoff + i * 64);
+    x[i % FN] = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    sx[i % FN] = *reinterpret_cast<const int*>(lds + st + sxoff + i * 64);
   };
   auto read_w = [&](uint32_t st) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = j < kFragW ? 4 * j : kCols + 4 * (j - kFragW);
+    for (int j = 0; j < FN; ++j) {
+      const int row = j < kFragW ? frag_col(0, j) : kCols + frag_col(0, j - kFragW);
       w_next[j] = *reinterpret_cast<const i32x4*>(lds + st + boff + row * (kStep / 2));
       sw_next[j] = *reinterpret_cast<const int*>(lds + st + swoff + row * 4);
     }
   };
   auto take_w = [&] {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < FN; ++j) {
       w[j] = w_next[j];
       sw[j] = sw_next[j] >> (8 * q);   // the lane group's block
     }
   };
   auto multiply = [&](int i, auto first, auto reads) {
-    const int s = sx[i % 4] >> (8 * q);
+    const int s = sx[i % FN] >> (8 * q);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < FN; ++j) {
       const i32x8 wf = {w[j][0], w[j][1], w[j][2], w[j][3], 0, 0, 0, 0};
       const f32x4 c = decltype(first)::value ? f32x4{} : acc[i][j];
       acc[i][j] =
-          __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, x[i % 4], c, 4, 0, 0, sw[j], 0, s);
+          __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, x[i % FN], c, 4, 0, 0, sw[j], 0, s);
     }
     // keeps the MFMAs where they stand among the reads, waits and barriers (they
     // touch no memory, so the compiler would sink them all behind the branches)
-    asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]), "+v"(acc[i][2]), "+v"(acc[i][3]));
+    pin<FN>(acc[i]);
     // the matrix cores first, `reads` LDS reads behind each MFMA
     if constexpr (decltype(reads)::value > 0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < FN; ++j) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x100, decltype(reads)::value, 0);
       }
@@ -455,7 +473,7 @@ __global__ __launch_bounds__(C::NT, C::PER_CU * C::NW / 4) void mx_rows_kernel(M
 
   // ---- the stream
   // A step's fills go out a few at a time between its MFMAs (all at once they
-  // queue behind each other while the matrix cores idle): places 0 and 1 behind
+  // queue behind each other while the matrix cores idle): the first P behind
   // the join that frees the slot, the others in the next step, before its join.
   constexpr int kEach = (C::kPer + FM - 1) / FM;   // fills of a place
   auto fills = [&](auto place, int slot) {
@@ -477,16 +495,19 @@ __global__ __launch_bounds__(C::NT, C::PER_CU * C::NW / 4) void mx_rows_kernel(M
     for_each_place<FM>([&](auto place) { fills(place, s); });
     advance();
   }
-  fills(std::integral_constant<int, 0>{}, NST - 1);
-  fills(std::integral_constant<int, 1>{}, NST - 1);
+  for_each_place<P>([&](auto place) { fills(place, NST - 1); });
   wait_vm<0>();
   join();
   read_w(0);
-  read_x(0, 0, 0);
-  read_x(0, 1, 1);
+#pragma unroll
+  for (int i = 0; i < P; ++i) read_x(0, i);
   take_w();
   int slot = 0, filling = NST - 1;
-  // One step.  Its last two row fragments run behind the join: by then it has
+  // fills and stores newer than the fills that a tile's first step waits for (a
+  // larger count than the instruction holds: it waits for a little more)
+  constexpr int kStored =
+      std::min(63, (NST - 2) * C::kPer + tile_stores<MODE, C, OUT>());
+  // One step.  Its last P row fragments run behind the join: by then it has
   // been read by all (their operands are in registers) and the next step has
   // landed for all; the step NST on is filled in its place.  `stored`: the
   // stores of the tile before are newer than the fills that are waited for.
@@ -494,24 +515,30 @@ __global__ __launch_bounds__(C::NT, C::PER_CU * C::NW / 4) void mx_rows_kernel(M
     const uint32_t st = slot * C::kStage;
     const int next = slot + 1 == NST ? 0 : slot + 1;
     const uint32_t sn = next * C::kStage;
-    for_each_place<FM - 2>([&](auto place) {
+    for_each_place<FM - P>([&](auto place) {
       constexpr int i = decltype(place)::value;
-      read_x(st, i + 2, (i + 2) % 4);
-      fills(std::integral_constant<int, i + 2>{}, filling);
+      read_x(st, i + P);
+      fills(std::integral_constant<int, i + P>{}, filling);
       multiply(i, first, std::integral_constant<int, 1>{});
     });
     advance();
-    if (decltype(first)::value && stored) wait_vm<(NST - 2) * C::kPer + tile_stores<MODE, C, OUT>()>();
+    if (decltype(first)::value && stored) wait_vm<kStored>();
     else wait_vm<(NST - 2) * C::kPer>();
     join();
     filling = slot;
     read_w(sn);
-    read_x(sn, 0, FM % 4);
-    read_x(sn, 1, (FM + 1) % 4);
-    fills(std::integral_constant<int, 0>{}, filling);
-    multiply(FM - 2, first, std::integral_constant<int, 4>{});
-    fills(std::integral_constant<int, 1>{}, filling);
-    multiply(FM - 1, first, std::integral_constant<int, 0>{});
+    for_each_place<P>([&](auto place) {
+      constexpr int i = decltype(place)::value;
+      // the next step's column fragments behind the first group, its row fragments
+      // behind the second (all behind the first where there are two)
+      if constexpr (i == (P > 2)) {
+#pragma unroll
+        for (int u = 0; u < P; ++u) read_x(sn, u);
+      }
+      fills(place, filling);
+      constexpr int kReads = P > 2 ? (i < 2 ? 2 : 0) : (i < 1 ? 4 : 0);
+      multiply(FM - P + i, first, std::integral_constant<int, kReads>{});
+    });
     take_w();
     slot = next;
   };
@@ -519,16 +546,15 @@ __global__ __launch_bounds__(C::NT, C::PER_CU * C::NW / 4) void mx_rows_kernel(M
   // tile of 128 rows of 256 then costs 4% to 15% less; skipping single row fragments
   // breaks up the reads between the MFMAs and costs full tiles 5%).
   auto pass = [&](bool stored) {
-    for_each_place<FM - 2>([&](auto place) {
-      fills(std::integral_constant<int, decltype(place)::value + 2>{}, filling);
+    for_each_place<FM - P>([&](auto place) {
+      fills(std::integral_constant<int, decltype(place)::value + P>{}, filling);
     });
     advance();
-    if (stored) wait_vm<(NST - 2) * C::kPer + tile_stores<MODE, C, OUT>()>();
+    if (stored) wait_vm<kStored>();
     else wait_vm<(NST - 2) * C::kPer>();
     join();
     filling = slot;
-    fills(std::integral_constant<int, 0>{}, filling);
-    fills(std::integral_constant<int, 1>{}, filling);
+    for_each_place<P>([&](auto place) { fills(place, filling); });
     slot = slot + 1 == NST ? 0 : slot + 1;
   };
   for (int it = 0; it < n_items; ++it) {
@@ -537,8 +563,8 @@ __global__ __launch_bounds__(C::NT, C::PER_CU * C::NW / 4) void mx_rows_kernel(M
       for (int kt = 0; kt < nk; ++kt) pass(it > 0 && kt == 0);
       const uint32_t st = slot * C::kStage;
       read_w(st);
-      read_x(st, 0, 0);
-      read_x(st, 1, 1);
+#pragma unroll
+      for (int i = 0; i < P; ++i) read_x(st, i);
       take_w();
     } else {
       step(std::integral_constant<bool, true>{}, it > 0);
@@ -581,6 +607,23 @@ hipError_t run_rows(MxArgs g, const moe_dims& dm, hipStream_t s) {
 bool use_big(const moe_dims& dm, int64_t cols, int64_t K) {
   const int64_t R = dm.T * dm.k;
   return R / Big::BM * ((cols + Big::BN - 1) / Big::BN) >= 128 && R >= 128 * dm.E && K >= 512;
+}
+
+// The down product's large tile with four wavefronts instead of eight: 40% fewer LDS
+// reads for a product, but one wavefront to a SIMD, whose stalls nothing fills.  us at
+// d = 2048, four wavefronts and eight: 64 experts of 1536 rows of 1024 233 and 258;
+// with the same first product, 8 experts of 2048 and 8192 rows 125 and 123, 384 and
+// 397; 256 experts of 256 and 512 rows 530 and 533, 878 and 892; at d = 1024, 32 experts
+// of 1024 and 4096 rows of 512 82 and 80, 237 and 246.
+bool use_wide(const moe_dims& dm) {
+  return dm.T * dm.k / Wide::BM * ((dm.d + Wide::BN - 1) / Wide::BN) >= 2048;
+}
+
+template <typename OUT>
+hipError_t run_down(const MxArgs& g, const moe_dims& dm, hipStream_t s) {
+  if (!use_big(dm, dm.d, dm.f)) return run_rows<DOWN, Small, OUT>(g, dm, s);
+  if (use_wide(dm)) return run_rows<DOWN, Wide, OUT>(g, dm, s);
+  return run_rows<DOWN, Big, OUT>(g, dm, s);
 }
 
 }  // namespace
@@ -630,10 +673,7 @@ hipError_t launch_down_mx(const moe_dims& dm, const void* hq, const uint8_t* h_s
   g.K = dm.f;
   g.N = dm.d;
   g.E = dm.E;
-  const bool big = use_big(dm, dm.d, dm.f);
-  if (dm.act == MOE_BF16)
-    return big ? run_rows<DOWN, Big, bf16_t>(g, dm, s) : run_rows<DOWN, Small, bf16_t>(g, dm, s);
-  return big ? run_rows<DOWN, Big, float>(g, dm, s) : run_rows<DOWN, Small, float>(g, dm, s);
+  return dm.act == MOE_BF16 ? run_down<bf16_t>(g, dm, s) : run_down<float>(g, dm, s);
 }
 
 }  // namespace moe
