@@ -202,3 +202,77 @@ def test_calls_refuse_other_devices_and_router_shapes():
     with pytest.raises(ValueError, match="stream must be on"):
         M.moe_rmsnorm(M.make_dims(8, 64, 4, 64, 2, torch.float32), x, None, x[0], 1e-6, None, x,
                       None, None, None, stream=Elsewhere())
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_a_layers_outputs_are_its_next_inputs(T):
+    """block after block through one layer's buffers: y and the stream are read before
+    they are overwritten"""
+    print(f"\n[case] serve chain {T}", flush=True)
+    rng = np.random.default_rng(7)
+    w = _weights(rng, 192, 8, 128, torch.bfloat16)
+    layer = MoEServeLayer(40, 192, 8, 128, 2, torch.bfloat16, few_slots=16)
+    layer.load(w["w1"], w["w3"], w["w2"])
+    y, stream = layer.forward(up(rng.normal(size=(T, 192)), torch.bfloat16), w["nw"], w["wr"],
+                              up(rng.normal(size=(T, 192)), torch.bfloat16))
+    x, res = y.clone(), stream.clone()
+    y2, stream2 = layer.forward(y, w["nw"], w["wr"], stream)
+    got = y2.clone(), stream2.clone()
+    y3, stream3 = layer.forward(x, w["nw"], w["wr"], res)
+    assert torch.equal(y3, got[0]) and torch.equal(stream3, got[1])
+    assert torch.equal(stream3, (x.float() + res.float()).to(torch.bfloat16))
+
+
+def test_two_layers_on_two_streams():
+    print("\n[case] serve two streams", flush=True)
+    rng = np.random.default_rng(9)
+    jobs = []
+    for T, d, E, f, k in ((300, 256, 16, 192, 4), (5, 512, 8, 256, 2)):
+        w = _weights(rng, d, E, f, torch.bfloat16)
+        layer = MoEServeLayer(T, d, E, f, k, torch.bfloat16)
+        layer.load(w["w1"], w["w3"], w["w2"])
+        x = up(rng.normal(size=(T, d)), torch.bfloat16)
+        y = layer.forward(x, w["nw"], w["wr"])[0].clone()
+        jobs.append((layer, x, w, y, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for layer, *_ in jobs:
+            layer.y.zero_()
+        torch.cuda.synchronize()
+        for layer, x, w, _, stream in jobs:
+            with torch.cuda.stream(stream):
+                for _ in range(4):
+                    layer.forward(x, w["nw"], w["wr"])
+        torch.cuda.synchronize()
+        for layer, x, _, y, _ in jobs:
+            assert torch.equal(layer.y[:x.shape[0]], y)
+
+
+def test_training_step_with_its_norm_in_a_graph():
+    print("\n[case] layer pre_norm graph", flush=True)
+    T, d, E, f, k = 1024, 256, 16, 256, 4
+    rng = np.random.default_rng(11)
+    w = _weights(rng, d, E, f, torch.bfloat16)
+    x, r, dy, ds = (up(rng.normal(size=(T, d)), torch.bfloat16) for _ in range(4))
+    layer = MoELayer(T, d, E, f, k, torch.bfloat16, pre_norm=True, gather=True, fold_gate=True)
+
+    def step():
+        layer.step(x, w["wr"], w["w1"], w["w3"], w["w2"], dy, norm_weight=w["nw"], residual=r,
+                   dsum=ds)
+
+    step()
+    torch.cuda.synchronize()
+    names = ("y", "stream", "dstream", "dnorm", "dx", "dw1", "dw3", "dw2", "dwr")
+    ref = {n: getattr(layer, n).clone() for n in names}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        for n in names:
+            getattr(layer, n).zero_()
+        layer.workspace.fill_(0xFF)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in names:
+            assert torch.equal(getattr(layer, n), ref[n]), n

@@ -699,7 +699,7 @@ def _enqueue(func, device, stream, *args):
             raise ValueError(f"stream must be on cuda:{device}, is on cuda:{stream.device_index}")
         raw = stream.cuda_stream
     fn = getattr(lib(), func)
-    if device == torch.cuda.current_device():
+    if device == torch._C._cuda_getDevice():
         st = fn(*args, raw)
     else:
         with torch.cuda.device(device):
