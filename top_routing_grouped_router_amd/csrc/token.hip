@@ -255,10 +255,11 @@ constexpr int operand_terms() {
 
 // The rows of one expert's weights (UP: of W1 and of W3) times its tokens: 64
 // weight rows per workgroup, 16 per wavefront, all of K; the tokens' operands
-// pass through LDS in batches of 512 k, which the four wavefronts share.  Two
-// register sets take turns, so that a batch's weights can be asked for before the
-// last one's are used up; asking a whole batch ahead needs more registers than
-// it saves time (29 against 22 us for the first product at 16 tokens).
+// pass through LDS in batches of 512 k, which the four wavefronts share.  Weights
+// asked for a whole batch ahead, or before the table is searched, need registers that
+// cost more wavefronts than the waits (29 and 30 against 22 us for the first product at
+// 16 tokens; 45 us in all).  One turn at a time leaves room for a fourth workgroup on a
+// CU, at 49 us (its waits are longer), and 6% less where experts have over 16 tokens.
 template <typename T, int MODE>
 __global__ __launch_bounds__(kThreads) void token_kernel(TokenArgs g) {
   constexpr int NM = MODE == UP ? 2 : 1, P = operand_terms<T, MODE>();
@@ -290,7 +291,6 @@ __global__ __launch_bounds__(kThreads) void token_kernel(TokenArgs g) {
     f32x4 acc[NM];
 #pragma unroll
     for (int m = 0; m < NM; ++m) acc[m] = f32x4{};
-    Weights<NM> wt[2];
     Piece<T, MODE, P> piece[kEach];
     auto load_x = [&](int batch) {
 #pragma unroll
@@ -300,9 +300,9 @@ __global__ __launch_bounds__(kThreads) void token_kernel(TokenArgs g) {
       }
     };
     load_x(0);
-    auto turn = [&](int batch, auto odd) {
-      constexpr int o = decltype(odd)::value;
-      wt[o].load(w, sc, K, batch);
+    auto turn = [&](int batch) {
+      Weights<NM> wt;
+      wt.load(w, sc, K, batch);
       __syncthreads();                                   // the last batch has been read
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
@@ -318,14 +318,15 @@ __global__ __launch_bounds__(kThreads) void token_kernel(TokenArgs g) {
       if (batch + 1 < batches) load_x(batch + 1);
       // the columns of tokens past the last take what lies there: a column of the
       // product depends on its own token alone, and they are not stored
-      multiply<NM, P>(wt[o], acc, [&](int p, int i) { return &xs[p][r][i ^ r]; });
+      multiply<NM, P>(wt, acc, [&](int p, int i) { return &xs[p][r][i ^ r]; });
     };
+    // two turns at once: the second one's weights are asked for during the first
     int batch = 0;
     for (; batch + 1 < batches; batch += 2) {
-      turn(batch, std::integral_constant<int, 0>{});
-      turn(batch + 1, std::integral_constant<int, 1>{});
+      turn(batch);
+      turn(batch + 1);
     }
-    if (batch < batches) turn(batch, std::integral_constant<int, 0>{});
+    if (batch < batches) turn(batch);
     // lane (r, q) holds weight rows 4 q + [0, 4) of token r
     if (t0 + r < n) {
       const int64_t to = list[t0 + r];
