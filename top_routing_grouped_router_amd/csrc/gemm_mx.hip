@@ -496,7 +496,7 @@ __global__ __launch_bounds__(C::NT, (C::PER_CU * C::NW + 3) / 4) void mx_rows_ke
     advance();
   }
   for_each_place<P>([&](auto place) { fills(place, NST - 1); });
-  wait_vm<0>();
+  wait_vm<(NST - 2) * C::kPer + std::min(P * kEach, C::kPer)>();   // the first step's
   join();
   read_w(0);
 #pragma unroll
