@@ -27,6 +27,22 @@ __host__ __device__ __forceinline__ int mx_scale_ld(int cols) { return (cols + 1
 // |v| as bits: ordered like the values, NaN above infinity
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
+// v of another lane, by a vector instruction (a shuffle goes through LDS and waits for
+// it: the norm of 16384 x 2048 takes 55 us with them, 50.5 so): the neighbour, the
+// neighbouring pair, the mirrored lane of 8 and of 16, the lane 4 and 8 along in 16
+enum LaneOf {
+  kSwap1 = 0xB1, kSwap2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140, kAlong4 = 0x124, kAlong8 = 0x128
+};
+template <int LANE, typename T>
+__device__ __forceinline__ T from_lane(T v) {
+  int w[sizeof(T) / 4];
+  __builtin_memcpy(w, &v, sizeof(T));
+#pragma unroll
+  for (int& i : w) i = __builtin_amdgcn_update_dpp(0, i, LANE, 0xF, 0xF, true);
+  __builtin_memcpy(&v, w, sizeof(T));
+  return v;
+}
+
 // scale byte of a block with the largest |value| bits `amax`
 template <int FMT>
 __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax) {
@@ -74,8 +90,9 @@ __device__ __forceinline__ uint32_t mx_store(const float (&v)[N], void* q) {
   uint32_t m = abs_bits(v[0]);
 #pragma unroll
   for (int i = 1; i < N; ++i) m = max(m, abs_bits(v[i]));
-#pragma unroll
-  for (int o = 1; o < 32 / N; o <<= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), o, 64)));
+  m = max(m, from_lane<kSwap1>(m));
+  m = max(m, from_lane<kSwap2>(m));
+  if constexpr (N == 4) m = max(m, from_lane<kMirror8>(m));
   const uint32_t s = mx_scale_byte<FMT>(m);
   const float inv = mx_inverse(s);
   float u[N];

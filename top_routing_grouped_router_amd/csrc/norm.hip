@@ -7,8 +7,8 @@
 // Squares are summed in fp32 by fours and those sums in 64 bits (an addition per four
 // values), y is an fp32 product rounded once to the act type, and the 8-bit rows are
 // the roundings of y itself, not of that product: near ties it is computed again with
-// what its roundings lost (16384 x 2048 rows: no element off instead of 24; 55.0 us
-// instead of 52.5, and 57.1 with every element computed so).
+// what its roundings lost (16384 x 2048 rows: no element off instead of 24, for 4%
+// more time, and 9% if every element were computed so).
 //   n = s rstd;  g = dy w;  dx = rstd (g - n mean(g n)) + dsum;  dw = sum_t dy n
 //
 // Every pass is bound by HBM: each tensor is read and written once, with the
@@ -17,9 +17,9 @@
 // four (fewer bytes per lane, so more rows under way), and rows longer than a
 // workgroup's registers are read twice (kWavePieces).
 //
-// Measured: 16384 x 2048 bf16 with residual, y and 8-bit rows (303 MB) 55.0 us, 5.5
-// TB/s (a large copy reaches 5.2); forward and backward there (470 MB) 103 us, of which
-// 48, 51 and 4 for the weight gradient's second step; one row of 2048 2.5 us.
+// Measured: 16384 x 2048 bf16 with residual, y and 8-bit rows (303 MB) 50.5 us, 6.0
+// TB/s (a large copy reaches 5.2); forward and backward there (470 MB) 97 us, of which
+// 44, 49 and 4 for the weight gradient's second step; one row of 2048 2.5 us.
 #include <algorithm>
 
 #include "mx.h"
@@ -30,11 +30,39 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 
+// v plus its value in the neighbouring 16 lanes (ROWS) or the other 32
+template <bool ROWS, typename F>
+__device__ __forceinline__ F swap_sum(F v) {
+  uint32_t a[sizeof(F) / 4], b[sizeof(F) / 4];
+  __builtin_memcpy(a, &v, sizeof(F));
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(F) / 4); ++i) {
+    const auto t = ROWS ? __builtin_amdgcn_permlane16_swap(a[i], a[i], false, false)
+                        : __builtin_amdgcn_permlane32_swap(a[i], a[i], false, false);
+    a[i] = t[0];
+    b[i] = t[1];
+  }
+  F x, y;
+  __builtin_memcpy(&x, a, sizeof(F));
+  __builtin_memcpy(&y, b, sizeof(F));
+  return x + y;
+}
+
+// the sum over the wavefront, the same in every lane
 template <typename F>
 __device__ __forceinline__ F wave_sum(F v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
+  v += from_lane<kSwap1>(v);
+  v += from_lane<kSwap2>(v);
+  v += from_lane<kMirror8>(v);
+  v += from_lane<kMirror16>(v);
+  return swap_sum<false>(swap_sum<true>(v));
+}
+
+// the sum over the lanes of the wavefront with the same lane % 4
+__device__ __forceinline__ float runs_sum(float v) {
+  v += from_lane<kAlong8>(v);
+  v += from_lane<kAlong4>(v);
+  return swap_sum<false>(swap_sum<true>(v));
 }
 
 // sum over the W wavefronts of a row (W = 1: the wavefront's own), the same in
@@ -82,7 +110,8 @@ __device__ __forceinline__ Rstd inverse_root(double m) {
 // 3 * 2^-24 |y| of it, at most 3 of its last places, so only a v that close to a tie
 // between elements, or to a scale's limit, can round to another element; these all
 // have 19 zero bits behind the first four of the significand.
-constexpr uint32_t kTieBits = 0x7FFFF, kTieNear = 4;
+constexpr int kTieShift = 32 - 19;
+constexpr uint32_t kTieNear = 4u << kTieShift;   // 4 last places, those bits at the top
 // y for those: to about 2^-45, rounded to odd, so that any later rounding to fewer
 // bits is that of the sum itself
 __device__ __forceinline__ float scaled_odd(float s, Rstd r, float w) {
@@ -152,10 +181,10 @@ __device__ __forceinline__ void piece_out(const NormArgs& g, int64_t row, int p,
   for (int i = 0; i < N; ++i) v[i] = s[i] * rstd.hi * w[i];
   if (g.y) st_nt16(reinterpret_cast<uint4*>(g.y) + row * per_row + p, pack16(v, T{}));
   if (g.q) {
-    uint32_t least = kTieBits;
+    uint32_t least = ~0u;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      least = min(least, (__float_as_uint(v[i]) + kTieNear) & kTieBits);
+      least = min(least, (__float_as_uint(v[i]) << kTieShift) + kTieNear);
     if (least <= 2 * kTieNear) {
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] = scaled_odd(s[i], rstd, w[i]);
@@ -441,13 +470,10 @@ __global__ __launch_bounds__(kThreads) void norm_dw_kernel(const float* part, in
     v.z += t.z;
     v.w += t.w;
   }
-#pragma unroll
-  for (int o = 4; o < 64; o <<= 1) {
-    v.x += __shfl_xor(v.x, o, 64);
-    v.y += __shfl_xor(v.y, o, 64);
-    v.z += __shfl_xor(v.z, o, 64);
-    v.w += __shfl_xor(v.w, o, 64);
-  }
+  v.x = runs_sum(v.x);
+  v.y = runs_sum(v.y);
+  v.z = runs_sum(v.z);
+  v.w = runs_sum(v.w);
   if ((threadIdx.x & 63) < 4) lds[threadIdx.x >> 6][c4] = v;
   __syncthreads();
   if (threadIdx.x < 4) {
