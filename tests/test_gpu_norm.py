@@ -221,7 +221,8 @@ def test_norm_backward(T, d, dtype, dsum):
 
 
 @pytest.mark.parametrize("T,d,dtype", [(523, 8256, torch.bfloat16), (523, 4160, torch.float32),
-                                       (129, 2112, torch.bfloat16), (513, 1024, torch.float32)])
+                                       (129, 2112, torch.bfloat16), (513, 1024, torch.float32),
+                                       (2051, 2048, torch.bfloat16), (511, 1600, torch.bfloat16)])
 def test_norm_backward_of_several_rows_each(T, d, dtype):
     """rows that take a workgroup, more of them than workgroups"""
     print(f"\n[case] norm backward several rows {T}x{d} {dtype}", flush=True)

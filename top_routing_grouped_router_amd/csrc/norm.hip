@@ -18,8 +18,8 @@
 // workgroup's registers are read twice (kWavePieces).
 //
 // Measured: 16384 x 2048 bf16 with residual, y and 8-bit rows (303 MB) 50.5 us, 6.0
-// TB/s (a large copy reaches 5.2); forward and backward there (470 MB) 97 us, of which
-// 44, 49 and 4 for the weight gradient's second step; one row of 2048 2.5 us.
+// TB/s (a large copy reaches 5.2); forward and backward there (470 MB) 93 us, of which
+// 44, 45 and 4 for the weight gradient's second step; one row of 2048 2.5 us.
 #include <algorithm>
 
 #include "mx.h"
@@ -502,11 +502,14 @@ unsigned row_grid(int64_t n) { return static_cast<unsigned>(std::min<int64_t>(n,
 
 // Pieces of a row per lane up to which the row belongs to one wavefront.  us, bf16,
 // forward / backward, a wavefront and a workgroup to a row:
-//   2 pieces: 16384 x 1024 28.7 / 30.5 and 33.4 / 47.7, 64 x 1024 5.7 / 7.9 and 4.9 / 8.0;
-//   4 pieces: 16384 x 2048 55.8 / 58.3 and 53.1 / 59.0, 2048 x 2048 9.6 / 20.3 and 8.3 / 16.1.
-// Rows in registers against rows read twice: 16384 x 4096 96 / 109 and 124 / 161, 8 pieces
-// to a lane of a workgroup 16384 x 16384 455 / 503 and 491 / 671.
+//   2 pieces: 16384 x 1024 29.0 / 28.4 and 32.6 / 43.7, 64 x 1024 5.6 / 6.7 and 5.0 / 6.4;
+//   4 pieces: 16384 x 2048 55.8 / 53.3 and 50.4 / 57.7, 512 x 2048 7.2 / 8.4 and 5.6 / 8.7,
+//   64 x 2048 6.7 / 7.5 and 5.1 / 6.6.
+// So the backward pass gives a wavefront 4 pieces too where there are rows enough.
+// Rows in registers against rows read twice: 16384 x 4096 99 / 108 and 127 / 163, 8 pieces
+// to a lane of a workgroup 16384 x 16384 445 / 495 and 492 / 687.
 constexpr int kWavePieces = 2;
+constexpr int64_t kWideWaveRows = 512;   // rows from which the backward pass takes 4
 
 template <typename T, int W, int NV>
 hipError_t run_norm(const NormArgs& g, hipStream_t s) {
@@ -544,6 +547,7 @@ hipError_t norm_bwd(const NormBwdArgs& a, int parts, hipStream_t s) {
   const int one = pieces_per_lane(pieces, 64), four = pieces_per_lane(pieces, 256);
   if (one && one <= kWavePieces)
     return one == 1 ? run_norm_bwd<T, 1, 1>(a, parts, s) : run_norm_bwd<T, 1, 2>(a, parts, s);
+  if (one == 4 && a.T >= kWideWaveRows) return run_norm_bwd<T, 1, 4>(a, parts, s);
   switch (four) {
     case 1: return run_norm_bwd<T, kWaves, 1>(a, parts, s);
     case 2: return run_norm_bwd<T, kWaves, 2>(a, parts, s);
@@ -574,7 +578,7 @@ hipError_t launch_rmsnorm(const moe_dims& dm, const void* x, const void* res, co
 // (their weight gradients are read again), of rows that take a whole workgroup at
 // least one: 64 rows of 4096 in bf16 10.8 -> 7.5 us; a row each also where there are
 // 512 costs 12.0 -> 15.6.  At 16384 x 2048, 256 and 1024 workgroups take as long as 512
-// (58, 61 and 58 us), at 16384 x 512 longer (25, 20 and 19).
+// (58, 61 and 58 us, a workgroup to a row), at 16384 x 512 longer (25, 20 and 19).
 int rmsnorm_bwd_parts(const moe_dims& dm) {
   const int pieces = dm.d / (dm.act == MOE_BF16 ? 8 : 4);
   const int64_t few = pieces <= 64 * kWavePieces ? 1 : 128;
