@@ -25,7 +25,7 @@
 //
 // Measured, d = 2048, 64 experts of 1024, k = 6, bf16: 1 token (20 MB of weights) 12.9 us
 // replayed, of which the two kernels 5.6 and 6.0: bound by latency (launch, the id,
-// the weights, one after another).  16 tokens (170 MB) 45 us: 22 us for the first
+// the weights, one after another).  16 tokens (170 MB) 44 us: 22 us for the first
 // product (5.0 TB/s, the rate of a copy), 17 for the second (3.4 TB/s: each workgroup's
 // 32 KB cost it a search and two batches' latencies), 5 for the combine.  Token
 // operands through the caches instead of LDS: 65 us (their loads, a few lanes
@@ -260,8 +260,10 @@ constexpr int operand_terms() {
 // cost more wavefronts than the waits (29 and 30 against 22 us for the first product at
 // 16 tokens; 45 us in all).  One turn at a time leaves room for a fourth workgroup on a
 // CU, at 49 us (its waits are longer), and 6% less where experts have over 16 tokens.
+// The second product of a bf16 layer fits four as it is (126 registers against 132:
+// 44.2 us, 118 against 122 at 128 tokens); the others would spill (54).
 template <typename T, int MODE>
-__global__ __launch_bounds__(kThreads) void token_kernel(TokenArgs g) {
+__global__ __launch_bounds__(kThreads, MODE == DOWN && sizeof(T) == 2 ? 4 : 1) void token_kernel(TokenArgs g) {
   constexpr int NM = MODE == UP ? 2 : 1, P = operand_terms<T, MODE>();
   constexpr int PH = operand_terms<T, DOWN>();
   __shared__ int list[MOE_TOKEN_MAX_SLOTS];
