@@ -637,7 +637,9 @@ moe_status moe_mx_dequantize(int64_t rows, int32_t cols, int32_t format, const v
  * overflows them: rstd 0).
  * x [T,d] act; residual [T,d] act or NULL (s = x); weight [d] fp32; eps >= 0.
  * sum [T,d] act or NULL: s.  It may be x or residual (in place).
- * y [T,d] act or NULL; it may be x when sum is not.
+ * y [T,d] act or NULL; it may be x or residual where sum is not that one.
+ * Otherwise the outputs share no memory with the inputs: rows are read and
+ * written in no order.
  * q [T,d] E4M3 and q_scale [T, moe_mx_scale_cols(d)], both or neither: the
  *   y before its rounding to act, quantised.  y or q has to be given.
  * rstd [T] fp32 or NULL (the backward pass reads it).

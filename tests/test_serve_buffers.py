@@ -1,0 +1,77 @@
+"""Host side of the serving layer's buffers (no GPU): the kernels are stood in for by
+a norm that takes its rows in either order, so that a row which is overwritten before
+it is read shows."""
+import numpy as np
+import pytest
+import torch
+
+from top_routing_grouped_router_amd import MoEServeLayer
+from top_routing_grouped_router_amd import _lib as L
+
+T, D, E, F, K = 12, 64, 4, 64, 2
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    def norm(dims, x, res, weight, eps, total, y, *rest):
+        given = [None if t is None else t.clone() for t in (x, res)]
+        want = given[0] if res is None else given[0] + given[1]
+        for order in (range(dims.T), reversed(range(dims.T))):
+            for t, was in zip((x, res), given):
+                if t is not None:
+                    t.copy_(was)
+            for t in order:
+                s = x[t].clone() if res is None else x[t] + res[t]
+                assert torch.equal(s, want[t]), f"row {t} was overwritten before it was read"
+                if total is not None:
+                    total[t] = s
+                y[t] = s * weight
+
+    def token(dims, x, *rest):
+        rest[8].copy_(x * 3)
+
+    monkeypatch.setattr(L, "moe_rmsnorm", norm)
+    monkeypatch.setattr(L, "moe_token_swiglu", token)
+    monkeypatch.setattr(L, "moe_route", lambda *a: None)
+
+
+def _layer():
+    layer = MoEServeLayer(T, D, E, F, K, torch.float32, device="cpu")
+    for t in (layer.norm_sum, layer.xn, layer.y):
+        t.zero_()
+    return layer
+
+
+def _normal(*shape):
+    return torch.from_numpy(np.random.default_rng(shape[0]).normal(size=shape)).float()
+
+
+@pytest.mark.parametrize("shift", [1, 5])
+@pytest.mark.parametrize("which", ["residual", "x", "both"])
+@pytest.mark.parametrize("of", ["norm_sum", "xn"])
+def test_rows_of_the_last_forward_at_other_places(calls, shift, which, of):
+    """a sequence has ended: the rows behind it move up, as slices of what the layer
+    gave out"""
+    layer = _layer()
+    weight, wr = torch.full((D,), 2.0), _normal(E, D)
+    layer.forward(_normal(T, D), weight, wr, _normal(T, D))
+    n = T - shift
+    old = getattr(layer, of)[shift:]
+    x = old if which != "residual" else _normal(n, D)
+    res = old if which != "x" else _normal(n, D)
+    want = x + res
+    y, stream = layer.forward(x, weight, wr, res)
+    assert torch.equal(stream, want) and torch.equal(y, want * 6)
+
+
+def test_the_same_rows_are_not_copied(calls):
+    layer = _layer()
+    weight, wr = torch.full((D,), 2.0), _normal(E, D)
+    _, stream = layer.forward(_normal(T, D), weight, wr, _normal(T, D))
+    seen = []
+    inner = L.moe_rmsnorm
+    L.moe_rmsnorm = lambda *a: (seen.append((a[1].data_ptr(), a[2].data_ptr())), inner(*a))
+    x, res = layer.y[:5], stream[:5]
+    want = x + res
+    _, got = layer.forward(x, weight, wr, res)
+    assert torch.equal(got, want) and seen == [(x.data_ptr(), layer.norm_sum.data_ptr())]

@@ -49,6 +49,21 @@ import torch
 from . import _lib as L
 
 
+def _shared(a, b):
+    """whether two tensors have memory in common"""
+    at, to = a.data_ptr(), b.data_ptr()
+    return a.numel() > 0 and b.numel() > 0 and at < to + b.nbytes and to < at + a.nbytes
+
+
+def _readable(t, outs):
+    """An input of the norm, or a copy of it.  The norm may write a row where it read it,
+    but rows of its outputs at other places (the sequences behind one that has ended)
+    may be overwritten before they are read."""
+    if t is not None and any(t.data_ptr() != o.data_ptr() and _shared(t, o) for o in outs):
+        return t.clone()
+    return t
+
+
 class MoELayer:
     def __init__(self, T: int, d: int, E: int, f: int, k: int, act: torch.dtype,
                  n_groups: int = 1, near_tie_eps: float = 1e-3, device="cuda",
@@ -280,7 +295,8 @@ class MoEServeLayer:
     Up to few_slots token-expert pairs go through moe_token_swiglu (activations
     in `act`, nothing sorted), more through the grouped products on 8-bit rows.
     The outputs are buffers that the next forward overwrites: one forward at a time,
-    on one stream or with its own ordering between them.
+    on one stream or with its own ordering between them.  They, and slices of them,
+    may be its inputs.
     """
 
     def __init__(self, max_tokens: int, d: int, E: int, f: int, k: int, act: torch.dtype,
@@ -346,6 +362,8 @@ class MoEServeLayer:
         stream = x if residual is None else self.norm_sum[:T]
         xn, y, idx, gate = self.xn[:T], self.y[:T], self.topk_idx[:T], self.topk_gate[:T]
         xq, xs = (None, None) if few else (self.xq[:T], self.x_scale[:T])
+        outs = (xn,) if residual is None else (xn, stream)
+        x, residual = _readable(x, outs), _readable(residual, outs)
         L.moe_rmsnorm(dims, x, residual, norm_weight, self.norm_eps,
                       None if residual is None else stream, xn, xq, xs, None)
         L.moe_route(dims, xn, wr, self.logits[:T], idx, gate, self.margin[:T], 0.0,
