@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from top_routing_grouped_router_amd import MoEServeLayer
+from top_routing_grouped_router_amd import MoELayer, MoEServeLayer
 
 from _lowp import up
 
@@ -68,3 +68,37 @@ def test_rows_that_move_up_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, ref))
+
+
+@pytest.mark.parametrize("T", [3, 300])
+def test_the_stream_outlives_the_outputs_that_it_was(T):
+    print(f"\n[case] serve y as input {T}", flush=True)
+    rng = np.random.default_rng(T)
+    layer, w = _serve(T, 192, 8, 128, 2, torch.bfloat16, 3)
+    y, _ = layer.forward(up(rng.normal(size=(T, 192)), torch.bfloat16), w["nw"], w["wr"])
+    for rows in (y, y[1:], layer.xn[:T], layer.xn[1:T]):
+        x = rows.clone()
+        want = layer.forward(x, w["nw"], w["wr"])[0].clone()
+        rows.copy_(x)
+        layer_y, stream = layer.forward(rows, w["nw"], w["wr"])
+        assert torch.equal(stream, x) and torch.equal(layer_y, want)
+
+
+@pytest.mark.parametrize("of", ["y", "xn"])
+def test_the_training_layers_outputs_as_its_input(of):
+    """gradients are of the input that was there, not of what the forward wrote there"""
+    print(f"\n[case] layer {of} as input", flush=True)
+    T, d, E, f, k = 128, 128, 8, 64, 2
+    rng = np.random.default_rng(4)
+    w = _weights(rng, d, E, f, torch.float32)
+    args = (w["wr"], w["w1"], w["w3"], w["w2"])
+    layer = MoELayer(T, d, E, f, k, torch.float32, pre_norm=True)
+    x, dy = (up(rng.normal(size=(T, d)), torch.float32) for _ in range(2))
+    layer.step(x, *args, dy, norm_weight=w["nw"])
+    ref = {n: getattr(layer, n).clone() for n in ("y", "dstream", "dnorm", "dwr")}
+    own = getattr(layer, of)
+    own.copy_(x)
+    layer.step(own, *args, dy, norm_weight=w["nw"])
+    assert torch.equal(layer.stream, x)
+    for n, t in ref.items():
+        assert torch.equal(getattr(layer, n), t), n

@@ -75,3 +75,24 @@ def test_the_same_rows_are_not_copied(calls):
     want = x + res
     _, got = layer.forward(x, weight, wr, res)
     assert torch.equal(got, want) and seen == [(x.data_ptr(), layer.norm_sum.data_ptr())]
+
+
+@pytest.mark.parametrize("of", ["y", "xn"])
+@pytest.mark.parametrize("shift", [0, 3])
+def test_the_stream_outlives_the_outputs_that_it_was(calls, of, shift):
+    """rows of an output as the next input, without a residual: they are the stream
+    then, and not what the forward writes there"""
+    layer = _layer()
+    weight, wr = torch.full((D,), 2.0), _normal(E, D)
+    layer.forward(_normal(T, D), weight, wr, _normal(T, D))
+    x = getattr(layer, of)[shift:]
+    want = x.clone()
+    y, stream = layer.forward(x, weight, wr)
+    assert torch.equal(stream, want) and torch.equal(y, want * 6)
+
+
+def test_other_inputs_are_the_stream_themselves(calls):
+    layer = _layer()
+    x = _normal(3, D)
+    _, stream = layer.forward(x, torch.ones(D), _normal(E, D))
+    assert stream.data_ptr() == x.data_ptr()

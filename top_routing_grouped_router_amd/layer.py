@@ -142,7 +142,7 @@ class MoELayer:
                 self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         self.pre_norm = bool(pre_norm)
         self.norm_eps = float(norm_eps)
-        self.stream = None   # what was normed: the sum, or x without a residual
+        self.stream = None   # what was normed: the sum, or x
         self.norm_sum = empty(T, d, **ea) if self.pre_norm else None
         self.xn = empty(T, d, **ea) if self.pre_norm else None
         self.rstd = empty(T, **e32) if self.pre_norm else None
@@ -189,9 +189,12 @@ class MoELayer:
         """The pre-norm alone: the layer's input, from x and the residual."""
         if not self.pre_norm:
             raise ValueError("the layer was made without pre_norm")
-        self.stream = x if residual is None else self.norm_sum
-        L.moe_rmsnorm(self.dims, x, residual, norm_weight, self.norm_eps,
-                      None if residual is None else self.norm_sum, self.xn, None, None, self.rstd)
+        # x itself, unless the step writes there before the backward pass reads it
+        total = (self.norm_sum if residual is not None
+                 or any(_shared(x, t) for t in (self.xn, self.y, self.dx)) else None)
+        self.stream = x if total is None else total
+        L.moe_rmsnorm(self.dims, x, residual, norm_weight, self.norm_eps, total, self.xn, None,
+                      None, self.rstd)
         return self.xn
 
     def forward(self, x, wr, w1, w3, w2, routing=None, norm_weight=None, residual=None):
@@ -347,7 +350,8 @@ class MoEServeLayer:
 
     def forward(self, x, norm_weight, wr, residual=None):
         """x [T,d], T <= max_tokens: (y, stream), the experts' sum for norm(x +
-        residual) and x + residual (x itself without one)."""
+        residual) and x + residual (without one x itself, or a copy of it where x is
+        one of the layer's own outputs)."""
         T = x.shape[0]
         if x.dim() != 2 or x.shape[1] != self.d or T > self.T:
             raise ValueError(f"x must be [T, {self.d}] with T <= {self.T}, is {tuple(x.shape)}")
@@ -359,13 +363,15 @@ class MoEServeLayer:
     def _forward(self, x, norm_weight, wr, residual, T):
         R = T * self.k
         dims, few = self._dims(T), R <= self.few_slots
-        stream = x if residual is None else self.norm_sum[:T]
         xn, y, idx, gate = self.xn[:T], self.y[:T], self.topk_idx[:T], self.topk_gate[:T]
         xq, xs = (None, None) if few else (self.xq[:T], self.x_scale[:T])
-        outs = (xn,) if residual is None else (xn, stream)
+        # the stream is x itself without a residual, unless this forward writes there
+        total = (self.norm_sum[:T] if residual is not None or _shared(x, xn) or _shared(x, y)
+                 else None)
+        stream = x if total is None else total
+        outs = (xn,) if total is None else (xn, total)
         x, residual = _readable(x, outs), _readable(residual, outs)
-        L.moe_rmsnorm(dims, x, residual, norm_weight, self.norm_eps,
-                      None if residual is None else stream, xn, xq, xs, None)
+        L.moe_rmsnorm(dims, x, residual, norm_weight, self.norm_eps, total, xn, xq, xs, None)
         L.moe_route(dims, xn, wr, self.logits[:T], idx, gate, self.margin[:T], 0.0,
                     self.near_tie_count, 1, None, None, None, self.workspace)
         if few:
