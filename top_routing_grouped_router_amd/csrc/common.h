@@ -43,7 +43,9 @@ template <> struct Act<float> {
 template <> struct Act<bf16_t> {
   static __device__ __forceinline__ float load(const bf16_t* p) { return bf16_to_f32(*p); }
   static __device__ __forceinline__ float to_f32(bf16_t v) { return bf16_to_f32(v); }
-  static __device__ __forceinline__ bf16_t from_f32(float v) { return f32_to_bf16(v); }
+  static __device__ __forceinline__ bf16_t from_f32(float v) {   // any value, NaNs too
+    return static_cast<bf16_t>(bf16x2_rne(v, 0.0f));
+  }
   static constexpr int kPer16B = 8;
 };
 
