@@ -701,7 +701,8 @@ moe_status moe_expert_down_mx(const moe_dims* dims, const void* hq, const uint8_
  *   nothing.  The sum over slots is in slot order.
  * x [T,d] act; topk_idx, topk_gate [T,k]; weights and scales as in
  * moe_expert_up_mx and moe_expert_down_mx; y [T,d] act.  Products and sums are
- * fp32; between the products h keeps 16 significant bits (bf16 layers) or 24.
+ * fp32; between the products h is rounded to 16 significant bits (bf16 layers)
+ * or keeps its 24.
  * T * k <= MOE_TOKEN_MAX_SLOTS and d, f <= 2^20 (else MOE_ERR_UNSUPPORTED).
  * Workspace: moe_token_swiglu_workspace_bytes(dims) (not covered by
  * moe_workspace_bytes); 0 for dims that the call refuses, or T = 0.

@@ -15,9 +15,9 @@
 // A lane loads 16 bytes, one block of 32 codes of its weight row; the j-th
 // MFMA of the block takes k = 8 j + [0, 8) of it, so the token operand is read
 // at the same k.  fp32 activations are cut into three bf16 terms (8 bits each,
-// exactly), h into two in a bf16 layer (it is kept to 16 bits rather than
-// rounded to 8 between the two products) and three in an fp32 one; each term
-// is one more MFMA on the same weights.
+// exactly), h into two in a bf16 layer (it is rounded to 16 bits rather than to
+// 8 between the two products) and three in an fp32 one; each term is one more
+// MFMA on the same weights.
 //
 // A few tokens take two launches, in which each pair reads its expert by itself
 // and the second product sums a token's experts; more take three, in which each
@@ -64,7 +64,8 @@ struct TokenArgs {
 };
 
 // bf16 terms of fp32 values: the upper 8 significant bits each, the remainders
-// exact; infinities and NaNs stay in the first term alone
+// exact, the last one rounded to nearest even (three terms hold all 24 bits);
+// infinities and NaNs stay in the first term alone
 template <int P>
 __device__ __forceinline__ void terms(float v, bf16_t* out) {
   uint32_t u = __float_as_uint(v);
@@ -75,6 +76,7 @@ __device__ __forceinline__ void terms(float v, bf16_t* out) {
   for (int p = 1; p < P; ++p) {
     v -= __uint_as_float(u & 0xFFFF0000u);
     u = odd ? 0u : __float_as_uint(v);
+    if (p == P - 1) u += 0x7FFFu + ((u >> 16) & 1u);
     out[p] = static_cast<bf16_t>(u >> 16);
   }
 }
