@@ -633,8 +633,8 @@ moe_status moe_mx_dequantize(int64_t rows, int32_t cols, int32_t format, const v
  *
  *   s[t] = x[t] + residual[t], rounded to act;
  *   rstd[t] = 1 / sqrt(mean(s[t]^2) + eps);  y[t] = s[t] rstd[t] weight.
- * The norm is of s as stored.  Squares are fp32 (an |s| above about 1e19
- * overflows them: rstd 0).
+ * The norm is of s as stored.  Squares and their sum are 64 bits wide; rstd is
+ * rounded to fp32 (eps = 0: infinite for rows of zeros or below about 2^-128).
  * x [T,d] act; residual [T,d] act or NULL (s = x); weight [d] fp32; eps >= 0.
  * sum [T,d] act or NULL: s.  It may be x or residual (in place).
  * y [T,d] act or NULL; it may be x or residual where sum is not that one.

@@ -4,11 +4,11 @@
 //   s = round(x + r);  rstd = 1 / sqrt(mean(s^2) + eps);  y = (s rstd) w
 // The norm is taken of s as it is stored (rounded to the act type), so the
 // backward pass, which reads s, differentiates what the forward computed.
-// Squares are summed in fp32 by fours and those sums in 64 bits (an addition per four
-// values), y is an fp32 product rounded once to the act type, and the 8-bit rows are
-// the roundings of y itself, not of that product: near ties it is computed again with
-// what its roundings lost (16384 x 2048 rows: no element off instead of 24, for 4%
-// more time, and 9% if every element were computed so).
+// Squares are taken and summed in 64 bits, which HBM's time covers (16384 x 2048 bf16
+// with 8-bit rows: 50.4 us, as with fp32 squares), y is an fp32 product rounded once to
+// the act type, and the 8-bit rows are the roundings of y itself, not of that product:
+// near ties it is computed again with what its roundings lost (16384 x 2048 rows: no
+// element off instead of 24, for 4% more time, and 9% if every element were computed so).
 //   n = s rstd;  g = dy w;  dx = rstd (g - n mean(g n)) + dsum;  dw = sum_t dy n
 //
 // Every pass is bound by HBM: each tensor is read and written once, with the
@@ -82,13 +82,12 @@ __device__ __forceinline__ F row_sum(F v) {
   return v;
 }
 
-// sum += N squares: four at a time in fp32, whose error is a fraction of 2^-24 of the
-// whole row's sum
+// sum += N squares, in 64 bits: no value of fp32 overflows or vanishes, and what the
+// additions lose lies below what rstd's two floats hold
 template <int N>
 __device__ __forceinline__ double squares(const float* v, double sum) {
 #pragma unroll
-  for (int i = 0; i < N; i += 4)
-    sum += (v[i] * v[i] + v[i + 1] * v[i + 1]) + (v[i + 2] * v[i + 2] + v[i + 3] * v[i + 3]);
+  for (int i = 0; i < N; ++i) sum = fma(static_cast<double>(v[i]), static_cast<double>(v[i]), sum);
   return sum;
 }
 
@@ -109,7 +108,9 @@ __device__ __forceinline__ Rstd inverse_root(double m) {
 // The 8-bit rows are the roundings of y itself.  v = fl(fl(s rstd.hi) w) is within
 // 3 * 2^-24 |y| of it, at most 3 of its last places, so only a v that close to a tie
 // between elements, or to a scale's limit, can round to another element; these all
-// have 19 zero bits behind the first four of the significand.
+// have 19 zero bits behind the first four of the significand.  (Where rstd.lo, or
+// what a product of y loses, falls below fp32's range -- rows above 2^100, a y below
+// 2^-100 -- an element that close to a tie may be its other neighbour.)
 constexpr int kTieShift = 32 - 19;
 constexpr uint32_t kTieNear = 4u << kTieShift;   // 4 last places, those bits at the top
 // y for those: to about 2^-45, rounded to odd, so that any later rounding to fewer
