@@ -23,6 +23,7 @@
 #include <algorithm>
 
 #include "mx.h"
+#include "two_floats.h"
 
 namespace moe {
 namespace {
@@ -91,11 +92,8 @@ __device__ __forceinline__ double squares(const float* v, double sum) {
   return sum;
 }
 
-// 1 / sqrt(m) as the sum of two floats: the instruction's estimate (about 24 bits) and
-// a step of Newton's method, which doubles them
-struct Rstd {
-  float hi, lo;
-};
+// 1 / sqrt(m): the instruction's estimate (about 24 bits) and a step of Newton's
+// method, which doubles them
 __device__ __forceinline__ Rstd inverse_root(double m) {
   double r = __builtin_amdgcn_rsq(m);
   if (m > 0.0 && m < HUGE_VAL) r = fma(r, 0.5 * fma(-m * r, r, 1.0), r);
@@ -113,16 +111,6 @@ __device__ __forceinline__ Rstd inverse_root(double m) {
 // 2^-100 -- an element that close to a tie may be its other neighbour.)
 constexpr int kTieShift = 32 - 19;
 constexpr uint32_t kTieNear = 4u << kTieShift;   // 4 last places, those bits at the top
-// y for those: to about 2^-45, rounded to odd, so that any later rounding to fewer
-// bits is that of the sum itself
-__device__ __forceinline__ float scaled_odd(float s, Rstd r, float w) {
-  const float n = s * r.hi, en = fmaf(s, r.lo, fmaf(s, r.hi, -n));
-  const float y = n * w, ey = fmaf(en, w, fmaf(n, w, -y));
-  const float hi = y + ey, lo = (y - hi) + ey;
-  const uint32_t u = __float_as_uint(hi);
-  const int away = static_cast<int>(u ^ __float_as_uint(lo)) < 0 ? -1 : 1;
-  return __uint_as_float(lo != 0.0f && !(u & 1) ? u + away : u);
-}
 
 struct NormArgs {
   const void* x;
