@@ -102,3 +102,33 @@ def test_the_training_layers_outputs_as_its_input(of):
     assert torch.equal(layer.stream, x)
     for n, t in ref.items():
         assert torch.equal(getattr(layer, n), t), n
+
+
+@pytest.mark.parametrize("T", [3, 300])
+def test_a_layer_without_weights_gives_nan(T):
+    print(f"\n[case] serve before load {T}", flush=True)
+    for _ in range(2):   # memory that held other weights
+        layer, w = _serve(T, 128, 8, 64, 2, torch.bfloat16, 3)
+        del layer
+        layer = MoEServeLayer(T, 128, 8, 64, 2, torch.bfloat16)
+        y, _ = layer.forward(up(np.ones((T, 128)), torch.bfloat16), w["nw"], w["wr"])
+        assert torch.isnan(y).all()
+
+
+def test_weights_loaded_on_another_stream_stay():
+    print("\n[case] serve load on a stream", flush=True)
+    layer, w = _serve(5, 512, 64, 512, 2, torch.bfloat16, 6)
+    x = up(np.random.default_rng(0).normal(size=(5, 512)), torch.bfloat16)
+    ref = layer.forward(x, w["nw"], w["wr"])[0].clone()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    busy = torch.zeros(1 << 28, device="cuda")
+    for _ in range(3):
+        for _ in range(8):
+            busy.add_(1)   # the current stream is behind
+        other = MoEServeLayer(5, 512, 64, 512, 2, torch.bfloat16)
+        with torch.cuda.stream(side):
+            other.load(w["w1"], w["w3"], w["w2"])
+            y = other.forward(x, w["nw"], w["wr"])[0].clone()
+        torch.cuda.synchronize()
+        assert torch.equal(y, ref)

@@ -96,3 +96,22 @@ def test_other_inputs_are_the_stream_themselves(calls):
     x = _normal(3, D)
     _, stream = layer.forward(x, torch.ones(D), _normal(E, D))
     assert stream.data_ptr() == x.data_ptr()
+
+
+def test_weights_are_nan_until_they_are_loaded():
+    """a scale byte of 255 makes its block NaN, whatever the elements"""
+    layer = _layer()
+    for name in ("w1", "w3", "w2"):
+        assert (getattr(layer, name + "_scale") == 255).all()
+
+
+@pytest.mark.parametrize("bad", ["w1", "w3", "w2"])
+def test_load_takes_all_weights_or_none(monkeypatch, bad):
+    done = []
+    monkeypatch.setattr(L, "moe_mx_quantize", lambda *a: done.append(a))
+    layer = _layer()
+    w = {"w1": torch.zeros(E, F, D), "w3": torch.zeros(E, F, D), "w2": torch.zeros(E, D, F)}
+    w[bad] = w[bad][:, :, 1:]
+    with pytest.raises(ValueError, match=bad):
+        layer.load(**w)
+    assert not done

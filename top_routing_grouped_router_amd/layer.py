@@ -322,6 +322,10 @@ class MoEServeLayer:
         self.w1, self.w1_scale = empty(E, f, d // 2, dtype=u8), empty(E, f, ld, dtype=u8)
         self.w3, self.w3_scale = empty(E, f, d // 2, dtype=u8), empty(E, f, ld, dtype=u8)
         self.w2, self.w2_scale = empty(E, d, f // 2, dtype=u8), empty(E, d, lf, dtype=u8)
+        for scale in (self.w1_scale, self.w3_scale, self.w2_scale):
+            scale.fill_(255)   # NaN, until there are weights
+        if self.w1_scale.is_cuda and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.w1_scale.device).synchronize()   # load may run on any
         self.norm_sum, self.xn, self.y = (empty(T, d, dtype=act) for _ in range(3))
         self.xq, self.x_scale = empty(T, d, dtype=u8), empty(T, ld, dtype=u8)
         self.hq, self.h_scale = empty(R, f, dtype=u8), empty(R, lf, dtype=u8)
@@ -340,12 +344,14 @@ class MoEServeLayer:
         return L.make_dims(T, self.d, self.E, self.f, self.k, self.act)
 
     def load(self, w1, w3, w2):
-        """Quantises the expert weights, [E,f,d], [E,f,d] and [E,d,f] in fp32 or bf16."""
-        for w, name, shape in ((w1, "w1", (self.E, self.f, self.d)),
-                               (w3, "w3", (self.E, self.f, self.d)),
-                               (w2, "w2", (self.E, self.d, self.f))):
+        """Quantises the expert weights, [E,f,d], [E,f,d] and [E,d,f] in fp32 or bf16
+        (until then every y is NaN)."""
+        weights = {"w1": w1, "w3": w3, "w2": w2}
+        for name, w in weights.items():
+            shape = (self.E, self.d, self.f) if name == "w2" else (self.E, self.f, self.d)
             if tuple(w.shape) != shape:
                 raise ValueError(f"{name} must be {shape}, is {tuple(w.shape)}")
+        for name, w in weights.items():
             L.moe_mx_quantize(w, "e2m1", getattr(self, name), getattr(self, name + "_scale"))
 
     def forward(self, x, norm_weight, wr, residual=None):
