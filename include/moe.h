@@ -94,6 +94,12 @@ const char* moe_last_error(void);
  * are invalid. */
 size_t moe_workspace_bytes(const moe_dims* dims, int32_t n_groups);
 
+/* [host] Workspace bytes of a serving forward: what moe_route with one group
+ * and moe_permute need for up to dims->T tokens (moe_rmsnorm, the forward
+ * expert products and moe_combine need none, moe_token_swiglu has its own
+ * query).  Returns 0 when the dims are invalid. */
+size_t moe_serve_workspace_bytes(const moe_dims* dims);
+
 /* [host] Kernels that moe_expert_wgrad enqueues for these dims with
  * wgrad_dtype = act: 1 (one
  * kernel writes dW1, dW3, dW2), 2 (the expert rows are split into parts whose
@@ -705,7 +711,7 @@ moe_status moe_expert_down_mx(const moe_dims* dims, const void* hq, const uint8_
  * or keeps its 24.
  * T * k <= MOE_TOKEN_MAX_SLOTS and d, f <= 2^20 (else MOE_ERR_UNSUPPORTED).
  * Workspace: moe_token_swiglu_workspace_bytes(dims) (not covered by
- * moe_workspace_bytes); 0 for dims that the call refuses, or T = 0.
+ * moe_workspace_bytes or moe_serve_workspace_bytes); 0 for dims that the call refuses, or T = 0.
  */
 #define MOE_TOKEN_MAX_SLOTS 1024
 size_t moe_token_swiglu_workspace_bytes(const moe_dims* dims);   /* [host] */

@@ -132,3 +132,17 @@ def test_weights_loaded_on_another_stream_stay():
             y = other.forward(x, w["nw"], w["wr"])[0].clone()
         torch.cuda.synchronize()
         assert torch.equal(y, ref)
+
+
+@pytest.mark.parametrize("act", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,E,f,k,few", [(64, 256, 64, 8, 128), (128, 8, 64, 2, 1024), (64, 3, 64, 1, 0)])
+def test_forwards_stay_in_the_workspace(act, d, E, f, k, few):
+    print(f"\n[case] serve workspace {d} {E} {k} {act}", flush=True)
+    layer, w = _serve(3000, d, E, f, k, act, 8, few_slots=few)
+    n = layer.workspace.numel()
+    whole = torch.full((n + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    layer.workspace = whole[:n]
+    for T in (1, 15, 63, 64, 65, 1000, 3000):
+        x = up(np.random.default_rng(T).normal(size=(T, d)), act)
+        y, _ = layer.forward(x, w["nw"], w["wr"])
+        assert torch.isfinite(y).all() and (whole[n:] == 0xA5).all()

@@ -115,3 +115,19 @@ def test_load_takes_all_weights_or_none(monkeypatch, bad):
     with pytest.raises(ValueError, match=bad):
         layer.load(**w)
     assert not done
+
+
+def test_workspace_is_the_forwards_alone():
+    """not the training backward's: some percent of the 4-bit weights (214 MB here)"""
+    T, d, E, f, k = 16384, 2048, 64, 1024, 6
+    layer = MoEServeLayer(T, d, E, f, k, torch.bfloat16, device="meta")
+    dims = [L.make_dims(t, d, E, f, k, torch.bfloat16) for t in (1, 21, 63, 64, 4096, T)]
+    need = [L.moe_serve_workspace_bytes(dm) for dm in dims]
+    assert need == sorted(need) and 0 < need[0]
+    # routing sums and counts of 256 tiles, rows of E, and the permutation's of 64 blocks
+    assert need[-1] <= 2 * 256 * (E + 64) * 4
+    few = L.moe_token_swiglu_workspace_bytes(dims[1])
+    assert max(need[-1], few) <= layer.workspace.numel() < 4 << 20
+    assert need[-1] <= L.workspace_bytes(dims[-1])
+    assert L.moe_serve_workspace_bytes(L.make_dims(4, 96, 4, 64, 2, torch.bfloat16)) == 0
+    assert L.moe_serve_workspace_bytes(L.make_dims(0, 64, 4, 64, 2, torch.bfloat16)) > 0

@@ -49,6 +49,7 @@ EXPORTED = (
     "moe_route_noalloc_max_bytes", "moe_mx_scale_cols", "moe_mx_quantize", "moe_mx_dequantize",
     "moe_rmsnorm", "moe_rmsnorm_bwd", "moe_rmsnorm_bwd_workspace_bytes", "moe_expert_up_mx",
     "moe_expert_down_mx", "moe_token_swiglu", "moe_token_swiglu_workspace_bytes",
+    "moe_serve_workspace_bytes",
 )
 
 
@@ -125,6 +126,7 @@ _SIGNATURES = {
     "moe_route_flips": (_I32, [_I64, _I32, _I32, _P, _P, _P, _P, _P]),
     "moe_shuffle_plan": (_I32, [_I64, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _SZ,
                                 _P]),
+    "moe_serve_workspace_bytes": (_SZ, [_DIMS]),
     "moe_mx_scale_cols": (_I32, [_I32]),
     "moe_mx_quantize": (_I32, [_I64, _I32, _I32, _P, _I32, _P, _P, _P]),
     "moe_mx_dequantize": (_I32, [_I64, _I32, _I32, _P, _P, _I32, _P, _P]),
@@ -754,6 +756,11 @@ def moe_mx_dequantize(q, scale, fmt, dst, stream=None):
     """The values of q and scale into dst [..., cols] fp32 or bf16."""
     device, rows, cols, dtype, code, ptr, qp, sp = _mx_rows(dst, "dst", q, scale, fmt)
     _enqueue("moe_mx_dequantize", device, stream, rows, cols, code, qp, sp, dtype, ptr)
+
+
+def moe_serve_workspace_bytes(dims) -> int:
+    """Workspace of a forward of up to dims.T tokens: moe_route (one group) and moe_permute."""
+    return int(lib().moe_serve_workspace_bytes(ctypes.byref(dims)))
 
 
 def moe_rmsnorm(dims, x, residual, weight, eps, sum_out, y, q, q_scale, rstd, stream=None):

@@ -487,6 +487,13 @@ size_t moe_workspace_bytes(const moe_dims* dims, int32_t n_groups) {
   return workspace_needed(*dims, n_groups);
 }
 
+size_t moe_serve_workspace_bytes(const moe_dims* dims) {
+  if (check_dims(dims, __func__) != MOE_OK) return 0;
+  const moe_dims& dm = *dims;   // with one group the router's tile does not depend on T
+  return std::max(route_ws(dm, route_tile(dm.T, 1, dm.act), nullptr).bytes,
+                  perm_ws(dm.T, dm.E, nullptr).bytes);
+}
+
 size_t moe_grouped_swiglu_bwd_workspace_bytes(const moe_dims* dims, int32_t recompute) {
   if (check_dims(dims, __func__) != MOE_OK) return 0;
   return std::max(bwd_ws(*dims, nullptr, recompute != 0, false).bytes,

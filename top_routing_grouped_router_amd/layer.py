@@ -336,7 +336,7 @@ class MoEServeLayer:
         self.counts, self.offsets = empty(E, dtype=i32), empty(E + 1, dtype=i32)
         self.pos, self.src_token = empty(T, k, dtype=i32), empty(R, dtype=i32)
         few = self._dims(min(max_tokens, self.few_slots // k))
-        need = max(L.workspace_bytes(self._dims(max_tokens)),
+        need = max(L.moe_serve_workspace_bytes(self._dims(max_tokens)),
                    L.moe_token_swiglu_workspace_bytes(few), 256)
         self.workspace = empty(need, dtype=u8)
 
