@@ -131,3 +131,11 @@ def test_workspace_is_the_forwards_alone():
     assert need[-1] <= L.workspace_bytes(dims[-1])
     assert L.moe_serve_workspace_bytes(L.make_dims(4, 96, 4, 64, 2, torch.bfloat16)) == 0
     assert L.moe_serve_workspace_bytes(L.make_dims(0, 64, 4, 64, 2, torch.bfloat16)) > 0
+
+
+def test_a_router_on_another_device_is_refused(calls, monkeypatch):
+    """before anything runs: the router's call would read it there"""
+    monkeypatch.setattr(L, "moe_rmsnorm", lambda *a: pytest.fail("the norm ran"))
+    layer = _layer()
+    with pytest.raises(ValueError, match="wr must be on"):
+        layer.forward(_normal(3, D), torch.ones(D), torch.empty(E, D, device="meta"))

@@ -363,6 +363,8 @@ class MoEServeLayer:
             raise ValueError(f"x must be [T, {self.d}] with T <= {self.T}, is {tuple(x.shape)}")
         if tuple(wr.shape) != (self.E, self.d):
             raise ValueError(f"wr must be [{self.E}, {self.d}], is {tuple(wr.shape)}")
+        if wr.device != x.device:
+            raise ValueError(f"wr must be on {x.device}, is on {wr.device}")
         with torch.cuda.device_of(x):
             return self._forward(x, norm_weight, wr, residual, T)
 
