@@ -124,3 +124,17 @@ def test_graph_replays_and_streams(E):
     graph.replay()
     c.idx = other
     c.check()
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("T,d,E,f,k", [
+    (8, 128, 2, 1152, 2), (8, 128, 2, 1216, 2),     # on either side of the search
+    (2, 1024, 16, 512, 16), (3, 1024, 16, 512, 16), (4, 576, 4, 1024, 4), (6, 576, 4, 1024, 4),
+    (5, 64, 1, 4096, 1), (1, 128, 1, 16448, 1),
+])
+def test_up_to_8_tokens_of_few_experts(act, T, d, E, f, k):
+    print(f"\n[case] token few experts {T} {d} {E} {f} {k} {act}", flush=True)
+    c = Case(T, d, E, f, k, act, seed=T + f)
+    c.upload()
+    c.run()
+    c.check()

@@ -20,8 +20,8 @@
 // MFMA on the same weights.
 //
 // A few tokens take two launches, in which each pair reads its expert by itself
-// and the second product sums a token's experts; more take three, in which each
-// expert's weights are read once for all of its tokens (up to 16 at a time).
+// and the second product sums a token's experts (use_direct); more take three, in
+// which each expert's weights are read once for all of its tokens (up to 16 at a time).
 //
 // Measured, d = 2048, 64 experts of 1024, k = 6, bf16: 1 token (20 MB of weights) 12.9 us
 // replayed, of which the two kernels 5.6 and 6.0: bound by latency (launch, the id,
@@ -498,12 +498,20 @@ hipError_t run_rows(const TokenArgs& g, int N, unsigned ny, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Tokens up to which each pair reads its expert by itself.  us of the call, so /
-// with the search of the table, replayed: d = 2048, f = 1024, 64 experts, k = 6: 1 token
-// 12.9 / 20.6, 8 tokens 35.3 / 40.2, 12 tokens 49.6 / 46.0; 8 experts of 2048, k = 2: 8
-// tokens 26.6 / 25.5, 12 tokens 35.9 / 26.2; d = 768, 16 experts of 512, k = 2: 8 tokens
-// 10.8 / 13.9, 24 tokens 20.0 / 16.3.
-constexpr int64_t kDirectTokens = 8;
+// Each pair reads its expert by itself: up to 8 tokens, while experts that several pairs
+// share are not read too often (what more than one read of them costs grows with d f,
+// what two launches and no search save with d).  us of the call, so / with the search
+// of the table, replayed: d = 2048, f = 1024, 64 experts, k = 6: 1 token 13.0 / 20.8, 8
+// tokens 36.2 / 38.5, 12 tokens 49.5 / 45.0; 4 experts, k = 4: 4 tokens 18.0 / 21.5, 6
+// tokens 22.8 / 21.9, 8 tokens 27.7 / 23.0; f = 2048, 8 experts, k = 2: 6 tokens 22.3 /
+// 25.3, 8 tokens 27.2 / 25.9; d = 1024, f = 512, 16 experts, k = 16: 2 tokens 14.3 / 16.5,
+// 4 tokens 17.6 / 16.7, 8 tokens 26.4 / 18.4; f = 1024, k = 8: 3 tokens 15.6 / 17.4, 4
+// tokens 17.1 / 17.9 (searched), 6 tokens 23.4 / 18.6; d = 768, 16 experts of 512, k = 2:
+// 8 tokens 10.9 / 14.2, 24 tokens 20.1 / 16.5.
+bool use_direct(const moe_dims& dm) {
+  const int64_t R = dm.T * dm.k;
+  return dm.T <= 8 && (R - std::min<int64_t>(R, dm.E)) * dm.f < 16384;
+}
 
 int h_planes(const moe_dims& dm) { return dm.act == MOE_BF16 ? 2 : 3; }
 
@@ -540,7 +548,7 @@ hipError_t launch_token_swiglu(const moe_dims& dm, const void* x, const int32_t*
   g.scale[1] = w3_scale;
   const unsigned ny = static_cast<unsigned>(std::min(g.slots, dm.E));
   const bool bf = dm.act == MOE_BF16;
-  if (dm.T <= kDirectTokens) {
+  if (use_direct(dm)) {
     const dim3 up(dm.f / kRows, g.slots);
     if (bf) hipLaunchKernelGGL((token_up_kernel<bf16_t>), up, dim3(kThreads), 0, s, g);
     else hipLaunchKernelGGL((token_up_kernel<float>), up, dim3(kThreads), 0, s, g);
