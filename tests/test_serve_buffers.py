@@ -139,3 +139,22 @@ def test_a_router_on_another_device_is_refused(calls, monkeypatch):
     layer = _layer()
     with pytest.raises(ValueError, match="wr must be on"):
         layer.forward(_normal(3, D), torch.ones(D), torch.empty(E, D, device="meta"))
+
+
+@pytest.mark.parametrize("E,k,T,few", [
+    (8, 2, 16, True), (8, 2, 32, True), (8, 2, 33, False), (8, 2, 48, False), (8, 2, 64, False),
+    (4, 4, 16, True), (4, 4, 17, False), (4, 1, 32, True), (4, 1, 33, False),
+    (16, 16, 8, True), (16, 16, 9, False), (64, 6, 21, True), (64, 6, 22, False),
+    (256, 8, 16, True), (256, 8, 17, False)])
+def test_few_tokens_by_pairs_and_experts(calls, monkeypatch, E, k, T, few):
+    """which products a forward takes: by the pairs, and by the pairs of an expert"""
+    made = []
+    for name in ("moe_permute", "moe_expert_up_mx", "moe_expert_down_mx", "moe_combine"):
+        monkeypatch.setattr(L, name, lambda *a, name=name: made.append(name))
+    x, wr = _normal(T, D), _normal(E, D)
+    for given, want in ((None, few), (T * k, True), (T * k - 1, False), (0, False)):
+        kw = {} if given is None else {"few_slots": given}
+        layer = MoEServeLayer(T, D, E, F, k, torch.float32, device="cpu", **kw)
+        made.clear()
+        layer.forward(x, torch.ones(D), wr)
+        assert (not made) == want, (given, made)

@@ -295,22 +295,20 @@ class MoELayer:
 class MoEServeLayer:
     """The layer's forward with 4-bit expert weights, for up to max_tokens tokens.
 
-    Up to few_slots token-expert pairs go through moe_token_swiglu (activations
-    in `act`, nothing sorted), more through the grouped products on 8-bit rows.
+    A few token-expert pairs go through moe_token_swiglu (activations in `act`,
+    nothing sorted), more through the grouped products on 8-bit rows.  few_slots is
+    how many; without it the layer takes what is faster, as measured.
     The outputs are buffers that the next forward overwrites: one forward at a time,
     on one stream or with its own ordering between them.  They, and slices of them,
     may be its inputs.
     """
 
     def __init__(self, max_tokens: int, d: int, E: int, f: int, k: int, act: torch.dtype,
-                 norm_eps: float = 1e-6, few_slots: int = 128, device="cuda"):
+                 norm_eps: float = 1e-6, few_slots=None, device="cuda"):
         self.T, self.d, self.E, self.f, self.k, self.act = max_tokens, d, E, f, k, act
         self.norm_eps = float(norm_eps)
-        # us of a forward, grouped products / moe_token_swiglu: d = 2048, 64 experts of
-        # 1024, k = 6: 24 pairs 69 / 54, 126 pairs 89 / 86, 252 pairs 89 / 95; 8 experts of
-        # 2048, k = 2: 48 pairs 59 / 53, 96 pairs 61 / 71; d = 256, 16 experts of 256, k = 4:
-        # 128 pairs 32 / 25, 384 pairs 33 / 37
-        self.few_slots = min(int(few_slots), L.MOE_TOKEN_MAX_SLOTS)
+        self.by_expert = few_slots is None
+        self.few_slots = min(128 if self.by_expert else int(few_slots), L.MOE_TOKEN_MAX_SLOTS)
         dev = torch.device(device)
         T, R = max(max_tokens, 1), max(max_tokens * k, 1)
 
@@ -343,6 +341,21 @@ class MoEServeLayer:
     def _dims(self, T):
         return L.make_dims(T, self.d, self.E, self.f, self.k, self.act)
 
+    def _few(self, T):
+        """Whether T tokens go through moe_token_swiglu.
+
+        It reads an expert's weights once for every 16 of its pairs, of which there are
+        at most T, and T k / E on average.  us of a forward, grouped products /
+        moe_token_swiglu, bf16: d = 2048, 64 experts of 1024, k = 6: 24 pairs 68 / 54, 126 pairs 88 / 86,
+        192 pairs 88 / 90; 8 experts of 2048, k = 2: 64 pairs 59 / 54, 96 pairs 61 / 71;
+        4 experts of 1024, k = 4: 64 pairs 52 / 49, 96 pairs 53 / 62; k = 1: 32 pairs
+        51 / 46, 64 pairs 52 / 60; d = 256, 16 experts of 256, k = 4: 128 pairs 32 / 25,
+        384 pairs 33 / 36; d = 1024, 16 experts of 512, k = 16: 128 pairs 53 / 40.  An fp32
+        layer's products take longer (d = 2048, 64 experts of 1024, k = 6: 48 pairs 187 /
+        176, 96 pairs 200 / 206) and keep fp32 rows."""
+        R = T * self.k
+        return R <= self.few_slots and (not self.by_expert or T <= 16 or R <= 8 * self.E)
+
     def load(self, w1, w3, w2):
         """Quantises the expert weights, [E,f,d], [E,f,d] and [E,d,f] in fp32 or bf16
         (until then every y is NaN)."""
@@ -370,7 +383,7 @@ class MoEServeLayer:
 
     def _forward(self, x, norm_weight, wr, residual, T):
         R = T * self.k
-        dims, few = self._dims(T), R <= self.few_slots
+        dims, few = self._dims(T), self._few(T)
         xn, y, idx, gate = self.xn[:T], self.y[:T], self.topk_idx[:T], self.topk_gate[:T]
         xq, xs = (None, None) if few else (self.xq[:T], self.x_scale[:T])
         # the stream is x itself without a residual, unless this forward writes there
