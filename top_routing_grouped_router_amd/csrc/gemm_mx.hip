@@ -366,7 +366,10 @@ __global__ __launch_bounds__(C::NT, (C::PER_CU * C::NW + 3) / 4) void mx_rows_ke
       }
     }
   };
-  // the u-th fill of the stream's next step, into ring slot `slot`
+  // The u-th fill of the stream's next step, into ring slot `slot`.  The sizes that are
+  // left for the step stay positive, as they must (a negative one would be read as about
+  // 4 GB, with kOutOfRange inside): a tile has rows, and columns (its column tile is below
+  // n_tiles_n, so n0 < N), and kt * kStep < K.
   auto fill = [&](auto which, int slot) {
     constexpr int u = decltype(which)::value;
     const uint32_t st = lds_base + slot * C::kStage;

@@ -3,8 +3,9 @@
 //
 // Both directions read and write each value once and are bound by HBM.  A lane
 // holds 16 bytes of the act tensor (8 bf16 or 4 fp32 values); a block's largest
-// value comes from 4 or 8 neighbouring lanes by shuffles, so loads and stores
-// stay coalesced (a lane per block would load at a 64- or 128-byte stride).
+// value comes from 4 or 8 neighbouring lanes by vector instructions (from_lane), so
+// loads and stores stay coalesced (a lane per block would load at a 64- or 128-byte
+// stride).
 // Lanes take 4 pieces each, a workgroup apart, to have 4 loads in flight: with 1, 2, 4
 // and 8 the quantisation of 134M bf16 values to e2m1 (340 MB) takes 58, 53, 53 and 54
 // us (6.4 TB/s), the way back 47, 47, 48 and 49 (7.1 TB/s: codes just written are read
