@@ -146,3 +146,18 @@ def test_forwards_stay_in_the_workspace(act, d, E, f, k, few):
         x = up(np.random.default_rng(T).normal(size=(T, d)), act)
         y, _ = layer.forward(x, w["nw"], w["wr"])
         assert torch.isfinite(y).all() and (whole[n:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("act", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T", [5, 20, 300])
+def test_a_bad_token_stays_alone(act, T):
+    """a NaN or an infinity in one sequence: the others get the bits they get without it"""
+    print(f"\n[case] serve bad token {T} {act}", flush=True)
+    layer, w = _serve(T, 128, 8, 64, 2, act, 5)
+    x, r = (up(np.random.default_rng(i).normal(size=(T, 128)), act) for i in (1, 2))
+    want, stream = (t.clone() for t in layer.forward(x, w["nw"], w["wr"], r))
+    x[1, 70], r[3, 5] = float("nan"), float("inf")
+    y, _ = layer.forward(x, w["nw"], w["wr"], r)
+    assert torch.isnan(y[1]).all() and not torch.isfinite(y[3]).any()
+    keep = [t for t in range(T) if t not in (1, 3)]
+    assert torch.equal(y[keep], want[keep])
