@@ -32,8 +32,8 @@
 // Measured at 98304 rows, d = 2048, 64 experts of 1024 (UP and DOWN together,
 // 1.24 TFLOP): one tile per workgroup 709 us; the persistent stream of tiles 650;
 // fills spread between the MFMAs instead of all behind the barrier 612; without the
-// MFMAs of wavefronts past a tile's rows 608; DOWN by wavefronts of 128 x 128, 588
-// (360 and 233 by themselves).  The MFMAs alone are 257 us at 2.4 GHz and about 300
+// MFMAs of wavefronts past a tile's rows 608; DOWN by wavefronts of 128 x 128, 577 to
+// 592 (by themselves 354 and 232, with fp32 outputs 306).  The MFMAs alone are 257 us at 2.4 GHz and about 300
 // at the clock that random data leaves.  What the rest is, by leaving out parts of the
 // loop: DOWN's 402 MB of stores cost it 75 us, UP's epilogue (the exponential and
 // reciprocal of silu, at a quarter of the vector rate, while the matrix cores idle)

@@ -23,8 +23,8 @@
 // and the second product sums a token's experts (use_direct); more take three, in
 // which each expert's weights are read once for all of its tokens (up to 16 at a time).
 //
-// Measured, d = 2048, 64 experts of 1024, k = 6, bf16: 1 token (20 MB of weights) 12.9 us
-// replayed, of which the two kernels 5.6 and 6.0: bound by latency (launch, the id,
+// Measured, d = 2048, 64 experts of 1024, k = 6, bf16: 1 token (20 MB of weights) 13.0 us
+// replayed, of which the two kernels 5.5 and 6.2: bound by latency (launch, the id,
 // the weights, one after another).  16 tokens (170 MB) 44 us: 22 us for the first
 // product (5.0 TB/s, the rate of a copy), 17 for the second (3.4 TB/s: each workgroup's
 // 32 KB cost it a search and two batches' latencies), 5 for the combine.  Token

@@ -346,13 +346,13 @@ class MoEServeLayer:
 
         It reads an expert's weights once for every 16 of its pairs, of which there are
         at most T, and T k / E on average.  us of a forward, grouped products /
-        moe_token_swiglu, bf16: d = 2048, 64 experts of 1024, k = 6: 24 pairs 68 / 54, 126 pairs 88 / 86,
-        192 pairs 88 / 90; 8 experts of 2048, k = 2: 64 pairs 59 / 54, 96 pairs 61 / 71;
-        4 experts of 1024, k = 4: 64 pairs 52 / 49, 96 pairs 53 / 62; k = 1: 32 pairs
-        51 / 46, 64 pairs 52 / 60; d = 256, 16 experts of 256, k = 4: 128 pairs 32 / 25,
-        384 pairs 33 / 36; d = 1024, 16 experts of 512, k = 16: 128 pairs 53 / 40.  An fp32
-        layer's products take longer (d = 2048, 64 experts of 1024, k = 6: 48 pairs 187 /
-        176, 96 pairs 200 / 206) and keep fp32 rows."""
+        moe_token_swiglu, bf16: d = 2048, 64 experts of 1024, k = 6: 24 pairs 68 / 54,
+        126 pairs 88 / 86, 192 pairs 88 / 90; 8 experts of 2048, k = 2: 64 pairs 59 /
+        54, 96 pairs 61 / 71; 4 experts of 1024, k = 4: 64 pairs 52 / 49, 96 pairs 53 /
+        62; k = 1: 32 pairs 51 / 46, 64 pairs 52 / 60; d = 256, 16 experts of 256, k =
+        4: 128 pairs 32 / 25, 384 pairs 33 / 36; d = 1024, 16 experts of 512, k = 16:
+        128 pairs 53 / 40.  An fp32 layer crosses earlier (d = 2048, 64 experts of 1024,
+        k = 6: 48 pairs 187 / 176, 96 pairs 200 / 206) but keeps fp32 rows for it."""
         R = T * self.k
         return R <= self.few_slots and (not self.by_expert or T <= 16 or R <= 8 * self.E)
 
