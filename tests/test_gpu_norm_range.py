@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 import torch
 
+import top_routing_grouped_router_amd as M
 from oracle import moe_oracle as O
 
 from _lowp import U32, U_ACT, host64, up, within
@@ -72,3 +73,22 @@ def test_elements_next_to_ties_of_any_rows(T, d, dtype):
     v = O.mx_element_values(o["q"].cpu().numpy(), "e4m3")
     bad = np.argwhere(v != want)
     assert not len(bad), (len(bad), bad[:5], v[tuple(bad[0])], want[tuple(bad[0])])
+
+
+@pytest.mark.parametrize("d", [256, 1024, 20032])
+@pytest.mark.parametrize("over", ["x", "residual"])
+@pytest.mark.parametrize("total", [False, True])
+def test_y_over_an_input(d, over, total):
+    """with the sum in the other input, in a tensor of its own, or nowhere"""
+    print(f"\n[case] norm y over {over} {total} d={d}", flush=True)
+    rng = np.random.default_rng(d)
+    x, r = (up(rng.normal(size=(40, d)), torch.bfloat16) for _ in range(2))
+    w = up(1 + 0.3 * rng.normal(size=d), torch.float32)
+    dims = M.make_dims(40, d, 1, 64, 1, torch.bfloat16)
+    ref = _run(x, r, w)
+    for own in ([False, True] if total else [False]):
+        a, b = x.clone(), r.clone()
+        y, other = (a, b) if over == "x" else (b, a)
+        s = None if not total else torch.empty_like(x) if own else other
+        M.moe_rmsnorm(dims, a, b, w, 1e-6, s, y, None, None, None)
+        assert torch.equal(y, ref["y"]) and (s is None or torch.equal(s, ref["sum"]))
